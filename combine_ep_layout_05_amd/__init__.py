@@ -28,6 +28,12 @@ EP_NOALLOC_SCRATCH_BYTES = 4 << 20
 EP_PAYLOAD_FP8_E4M3FN, EP_PAYLOAD_BF16 = 0, 1
 EP_STATUS_BAD_EXPERT_ID = 1
 PAYLOADS = {"fp8": EP_PAYLOAD_FP8_E4M3FN, "bf16": EP_PAYLOAD_BF16}
+EP_DTYPE_F32, EP_DTYPE_BF16 = 0, 1
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
+EP_ACT_NONE, EP_ACT_SILU_MUL = 0, 1
+ACTS = {"none": EP_ACT_NONE, "silu_mul": EP_ACT_SILU_MUL}
+SCALE_BLOCK = 128                      # columns per scale, of fp8 rows and 4-bit weights
 
 if not os.path.exists(LIB_PATH):
     raise ImportError("libep_mi355x.so is not built: run combine_ep_layout_05_amd/build.py "
@@ -35,6 +41,7 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 _P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_F = ctypes.c_float
 _SIGS = {
     "ep_layout_workspace_bytes": ([_I, _I, _I], _SZ),
     "ep_layout": ([_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
@@ -65,6 +72,11 @@ _SIGS = {
                                       + [_P, _SZ, _P, _P, _I, _I, _I, _P], _I),
     "ep_dedup_layout_dispatch_plan": ([_I, _I, _I, _I, _I, _I, _I, _I, _I, _P], _I),
     "ep_combine_reduce": ([_P, _P, _I, _I, _I, _P, _P], _I),
+    "ep_route": ([_P, _I, _I, _I, _I, _I, _P, _I, _F, _P, _P, _P], _I),
+    "ep_route_backward": ([_P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P], _I),
+    "ep_combine_backward": ([_P, _P, _P, _P, _I, _I, _I, _P, _P, _P], _I),
+    "ep_dispatch_backward": ([_P, _P, _I, _I, _I, _P, _P], _I),
+    "ep_expert_w4": ([_P, _P, _I, _I, _I, _P, _I, _P, _P, _I, _I, _P, _P], _I),
     "ep_strerror": ([_I], ctypes.c_char_p),
     "ep_last_hip_error": ([], _I),
 }
@@ -330,6 +342,171 @@ def ep_topk_idx_narrow(topk_idx64, out_i32, stream=None):
                                                          _ptr(out_i32), _stream(stream)))
 
 
+def _ptrs(stream, *tensors):
+    """The device pointers and the stream of one call, after checking that
+    everything lives on the current device (a kernel launched there could not
+    reach the others)."""
+    ptrs = [_ptr(t) for t in tensors]
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, dev))
+    if stream is not None and stream.device.index != dev:
+        raise ValueError("stream on %s, but the current device is cuda:%d" % (stream.device, dev))
+    return ptrs, _stream(stream)
+
+
+def _choice(value, table, name):
+    v = table.get(value, value)
+    if v not in table.values() or isinstance(v, bool):
+        raise ValueError("%s: one of %s expected, got %r" % (name, sorted(table), value))
+    return v
+
+
+def _logits(logits):
+    """(T, E, dtype code) of a matrix of router logits."""
+    _dt(logits, torch.float32, torch.bfloat16)
+    if logits.dim() != 2:
+        raise ValueError("logits: expected [T, E], got %s" % (tuple(logits.shape),))
+    T, E = logits.shape
+    return T, E, EP_DTYPE_BF16 if logits.dtype == torch.bfloat16 else EP_DTYPE_F32
+
+
+def ep_route(logits, topk_idx, topk_w, score="softmax", bias=None, renorm=True, scale=1.0,
+             stream=None):
+    """logits fp32 or bf16 [T, E] -> topk_idx int32 [T, K], topk_w fp32 [T, K].
+    score: "softmax" or "sigmoid"; bias: fp32 [E], added for the choice only
+    (sigmoid scores); renorm: divide by the sum over the choices."""
+    _dt(topk_idx, torch.int32)
+    _dt(topk_w, torch.float32)
+    _dt(bias, torch.float32)
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx: expected [T, K], got %s" % (tuple(topk_idx.shape),))
+    K = topk_idx.shape[1]
+    T, E, dtype = _logits(logits)
+    _matrix(topk_idx, (T, K), "topk_idx")
+    _matrix(topk_w, (T, K), "topk_w")
+    if bias is not None:
+        _matrix(bias, (E,), "bias")
+    score = _choice(score, SCORES, "score")
+    (pl, pb, pi, pw), s = _ptrs(stream, logits, bias, topk_idx, topk_w)
+    _check("ep_route", _lib.ep_route(pl, dtype, T, E, K, score, pb, int(bool(renorm)), scale, pi,
+                                     pw, s))
+
+
+def ep_route_backward(logits, topk_idx, grad_topk_w, grad_logits, score="softmax", renorm=True,
+                      scale=1.0, stream=None):
+    """grad_topk_w fp32 [T, K] -> grad_logits [T, E] (the logits' type), for the
+    choice topk_idx that ep_route made with the same score, renorm and scale."""
+    _dt(topk_idx, torch.int32)
+    _dt(grad_topk_w, torch.float32)
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx: expected [T, K], got %s" % (tuple(topk_idx.shape),))
+    K = topk_idx.shape[1]
+    T, E, dtype = _logits(logits)
+    _dt(grad_logits, logits.dtype)
+    _matrix(topk_idx, (T, K), "topk_idx")
+    _matrix(grad_topk_w, (T, K), "grad_topk_w")
+    _matrix(grad_logits, (T, E), "grad_logits")
+    score = _choice(score, SCORES, "score")
+    (pl, pi, pg, po), s = _ptrs(stream, logits, topk_idx, grad_topk_w, grad_logits)
+    _check("ep_route_backward", _lib.ep_route_backward(pl, dtype, T, E, K, score,
+                                                       int(bool(renorm)), scale, pi, pg, po, s))
+
+
+def ep_combine_backward(grad_out, expert_out, row_of_pair, topk_w, grad_expert_out, grad_topk_w,
+                        stream=None):
+    """grad_out bf16 [T, H] -> grad_expert_out bf16 [T*K, H] (the rows that
+    row_of_pair names; the rest stay as they are), grad_topk_w fp32 [T, K]."""
+    _dt(grad_out, *_BF16)
+    _dt(expert_out, *_BF16)
+    _dt(grad_expert_out, *_BF16)
+    _dt(row_of_pair, torch.int32)
+    _dt(topk_w, torch.float32)
+    _dt(grad_topk_w, torch.float32)
+    T, K = topk_w.shape
+    if grad_out.dim() != 2 or grad_out.shape[0] != T:
+        raise ValueError("grad_out: expected [%d, H], got %s" % (T, tuple(grad_out.shape)))
+    H = grad_out.shape[1]
+    _numel(row_of_pair, T * K, "row_of_pair")
+    _rows(expert_out, T * K, H, "expert_out")
+    _rows(grad_expert_out, T * K, H, "grad_expert_out")
+    _matrix(grad_topk_w, (T, K), "grad_topk_w")
+    (pg, py, pr, pw, po, pq), s = _ptrs(stream, grad_out, expert_out, row_of_pair, topk_w,
+                                        grad_expert_out, grad_topk_w)
+    _check("ep_combine_backward", _lib.ep_combine_backward(pg, py, pr, pw, T, H, K, po, pq, s))
+
+
+def ep_dispatch_backward(grad_recv, row_of_pair, grad_x, stream=None):
+    """grad_recv bf16 [T*K, H] (receive rows) -> grad_x bf16 [T, H]; K is
+    row_of_pair's entries per token."""
+    _dt(grad_recv, *_BF16)
+    _dt(grad_x, *_BF16)
+    _dt(row_of_pair, torch.int32)
+    if grad_x.dim() != 2:
+        raise ValueError("grad_x: expected [T, H], got %s" % (tuple(grad_x.shape),))
+    T, H = grad_x.shape
+    K = row_of_pair.numel() // T if T else 1
+    _numel(row_of_pair, T * K, "row_of_pair")
+    _rows(grad_recv, T * K, H, "grad_recv")
+    (pg, pr, px), s = _ptrs(stream, grad_recv, row_of_pair, grad_x)
+    _check("ep_dispatch_backward", _lib.ep_dispatch_backward(pg, pr, T, H, K, px, s))
+
+
+def ep_expert_w4(x, x_scales, expert_offset, w, w_scales, out, act="none", stream=None):
+    """The experts' products with 4-bit weights on receive rows in place.
+
+    x uint8 e4m3fn bytes [rows, C] with x_scales fp32 [rows, C/128], or bf16
+    [rows, C] with x_scales None; expert_offset int32 [E+1]; w uint8 e2m1 codes
+    [E, N, C/2] (even column in the low 4 bits), w_scales fp32 [E, N, C/128];
+    out bf16 [rows, D], N = D for act "none" and 2*D (gate rows, then up rows)
+    for "silu_mul".  Rows past expert_offset[E] stay as they are."""
+    _dt(x, torch.uint8, *_BF16)
+    _dt(expert_offset, torch.int32)
+    _dt(w, torch.uint8)
+    _dt(w_scales, torch.float32)
+    _dt(out, *_BF16)
+    act = _choice(act, ACTS, "act")
+    payload = EP_PAYLOAD_FP8_E4M3FN if x.dtype == torch.uint8 else EP_PAYLOAD_BF16
+    if x.dim() != 2 or out.dim() != 2 or w.dim() != 3:
+        raise ValueError("x [rows, C], out [rows, D] and w [E, N, C/2] expected")
+    (rows, cols), outs, E = x.shape, out.shape[1], w.shape[0]
+    _matrix(w, (E, 2 * outs if act == EP_ACT_SILU_MUL else outs, cols // 2), "w")
+    _matrix(w_scales, (E, w.shape[1], cols // SCALE_BLOCK), "w_scales")
+    _matrix(out, (rows, outs), "out")
+    _numel(expert_offset, E + 1, "expert_offset")
+    if payload == EP_PAYLOAD_FP8_E4M3FN:
+        _dt(x_scales, torch.float32)
+        _matrix(x_scales, (rows, cols // SCALE_BLOCK), "x_scales")
+    elif x_scales is not None:
+        raise ValueError("x_scales: bf16 rows have none")
+    (px, ps, po, pw, pv, pd), s = _ptrs(stream, x, x_scales, expert_offset, w, w_scales, out)
+    _check("ep_expert_w4", _lib.ep_expert_w4(px, ps, payload, rows, cols, po, E, pw, pv, outs, act,
+                                             pd, s))
+
+
+# The magnitudes of an e2m1 code's three low bits.
+_E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def w4_quantise(weight):
+    """weight [..., C] of any float type, C % 128 == 0 -> (codes uint8
+    [..., C/2], scales fp32 [..., C/128]) as ep_expert_w4 takes them: per 128
+    columns scale = amax / 6, codes the nearest e2m1 value of weight / scale,
+    ties to the even code.  Plain torch, for laying weights out once."""
+    if weight.shape[-1] % SCALE_BLOCK:
+        raise ValueError("weight: the last dimension must be a multiple of %d" % SCALE_BLOCK)
+    blocks = weight.float().unflatten(-1, (-1, SCALE_BLOCK))
+    scales = blocks.abs().amax(-1) / _E2M1[-1]
+    q = blocks / torch.where(scales > 0, scales, 1.0)[..., None]
+    mids = torch.tensor([(a + b) / 2 for a, b in zip(_E2M1, _E2M1[1:])], device=weight.device)
+    # at a midpoint between codes i and i+1 the even one is taken
+    code = torch.bucketize(q.abs(), mids, right=False)
+    tie = (code < 7) & (q.abs() == mids[code.clamp_max(6)]) & (code % 2 == 1)
+    code = (code + tie + 8 * torch.signbit(q)).to(torch.uint8).flatten(-2)
+    return code[..., 0::2] | (code[..., 1::2] << 4), scales
+
+
 def _tokens(buf, topk_idx):
     """The batch's token count, at most the buffers' T, from topk_idx [n, K]."""
     if topk_idx.dim() != 2 or topk_idx.shape[1] != buf.K or topk_idx.shape[0] > buf.T:
@@ -542,6 +719,8 @@ class EpBuffers:
             self.recv_x = torch.empty((T * K, H), dtype=torch.bfloat16, device=dev)
             self.recv_scales = None
         self.out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        self.topk_idx = torch.empty((T, K), **i32)       # what route() chooses
+        self.topk_w = torch.empty((T, K), dtype=torch.float32, device=dev)
 
     def _views(self, n):
         m = n * self.K
@@ -597,6 +776,88 @@ class EpBuffers:
         out = self.out[:self.n]
         ep_combine(expert_out, rop, topk_w, out, stream, self.geometry.get("combine"))
         return out
+
+    def route(self, logits, score="softmax", bias=None, renorm=True, scale=1.0, stream=None):
+        """logits fp32 or bf16 [n, E], n <= T -> (topk_idx[:n], topk_w[:n]) of
+        these buffers, as the layout and the combine take them (ep_route)."""
+        if logits.dim() != 2 or logits.shape[0] > self.T or logits.shape[1] != self.E:
+            raise ValueError("logits: expected [n, %d] with n <= %d, got %s" % (
+                self.E, self.T, tuple(logits.shape)))
+        n = logits.shape[0]
+        idx, w = self.topk_idx[:n], self.topk_w[:n]
+        ep_route(logits, idx, w, score, bias, renorm, scale, stream)
+        return idx, w
+
+    def combine_backward(self, grad_out, expert_out, topk_w, grad_expert_out=None,
+                         grad_topk_w=None, stream=None):
+        """The combine's gradient for the current batch: grad_out bf16 [n, H] ->
+        (grad_expert_out bf16 [n*K, H], grad_topk_w fp32 [n, K]).  Outputs not
+        given are allocated, grad_expert_out as zeros (rows without a pair are
+        not written); give them when the call is captured into a graph."""
+        _same_tokens(self, topk_w.shape[0], "topk_w")
+        _same_tokens(self, grad_out.shape[0], "grad_out")
+        if grad_expert_out is None:
+            grad_expert_out = torch.zeros_like(expert_out[:self.n * self.K])
+        if grad_topk_w is None:
+            grad_topk_w = torch.empty_like(topk_w)
+        ep_combine_backward(grad_out, expert_out, self._views(self.n)[0], topk_w, grad_expert_out,
+                            grad_topk_w, stream)
+        return grad_expert_out, grad_topk_w
+
+    def dispatch_backward(self, grad_recv, grad_x=None, stream=None):
+        """The dispatch's gradient for the current batch: grad_recv bf16
+        [>= n*K, H] -> grad_x bf16 [n, H] (allocated when not given)."""
+        if grad_x is None:
+            grad_x = torch.empty((self.n, self.H), dtype=torch.bfloat16, device=grad_recv.device)
+        _same_tokens(self, grad_x.shape[0], "grad_x")
+        ep_dispatch_backward(grad_recv, self._views(self.n)[0], grad_x, stream)
+        return grad_x
+
+
+class EpExpertsW4:
+    """The experts of an EpBuffers' batch with 4-bit weights: gate and up
+    products with SiLU(gate) * up, then the down product, on the receive rows
+    the dispatch wrote.  Holds the weights and the buffers for T tokens.
+
+        experts = EpExpertsW4(T, K, w_up, s_up, w_down, s_down)
+        buf.layout_dispatch(topk_idx, x)
+        out = buf.combine(experts(buf), topk_w)
+
+    w_up uint8 [E, 2*I, H/2] (gate rows, then up rows), s_up fp32 [E, 2*I,
+    H/128], w_down uint8 [E, H, I/2], s_down fp32 [E, H, I/128]: codes and
+    scales as w4_quantise lays them out; I % 128 == 0."""
+
+    def __init__(self, T, K, w_up, s_up, w_down, s_down):
+        for w, sc in ((w_up, s_up), (w_down, s_down)):
+            _dt(w, torch.uint8)
+            _dt(sc, torch.float32)
+        if w_up.dim() != 3 or w_down.dim() != 3:
+            raise ValueError("w_up [E, 2*I, H/2] and w_down [E, H, I/2] expected")
+        E, H, I = w_up.shape[0], w_up.shape[2] * 2, w_down.shape[2] * 2
+        if H % SCALE_BLOCK or I % SCALE_BLOCK:
+            raise ValueError("H = %d and I = %d must be multiples of %d" % (H, I, SCALE_BLOCK))
+        _matrix(w_up, (E, 2 * I, H // 2), "w_up")
+        _matrix(s_up, (E, 2 * I, H // SCALE_BLOCK), "s_up")
+        _matrix(w_down, (E, H, I // 2), "w_down")
+        _matrix(s_down, (E, H, I // SCALE_BLOCK), "s_down")
+        self.T, self.K, self.E, self.H, self.I = T, K, E, H, I
+        self.w_up, self.s_up, self.w_down, self.s_down = w_up, s_up, w_down, s_down
+        dev = w_up.device
+        self.mid = torch.empty((T * K, I), dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty((T * K, H), dtype=torch.bfloat16, device=dev)
+
+    def __call__(self, buf, stream=None):
+        """expert_out bf16 [n*K, H] for the current batch of `buf` (n <= T),
+        after its dispatch."""
+        if (buf.H, buf.K, buf.E) != (self.H, self.K, self.E) or buf.n > self.T:
+            raise ValueError("buffers of H, K, E = %s and %d tokens, experts of %s and up to %d" % (
+                (buf.H, buf.K, buf.E), buf.n, (self.H, self.K, self.E), self.T))
+        m = buf.n * self.K
+        _, _, rx, rs = buf._views(buf.n)
+        ep_expert_w4(rx, rs, buf.expert_offset, self.w_up, self.s_up, self.mid[:m], "silu_mul", stream)
+        ep_expert_w4(self.mid[:m], None, buf.expert_offset, self.w_down, self.s_down, self.out[:m],
+                     "none", stream)
+        return self.out[:m]
 
 
 class EpDedupBuffers:

@@ -39,6 +39,17 @@ bool dedup_ok(int T, int P)
     return T >= 0 && P >= 1 && P <= EP_MAX_DEDUP_PARTITIONS && (int64_t)T * P < ((int64_t)1 << 31);
 }
 
+// The checks ep_route and ep_route_backward share.
+int route_args(int dtype, int T, int E, int K, int score, int renorm, float scale)
+{
+    if (dtype != EP_DTYPE_F32 && dtype != EP_DTYPE_BF16) return EP_EINVAL;
+    if (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID) return EP_EINVAL;
+    if (renorm != 0 && renorm != 1) return EP_EINVAL;
+    if (!(scale - scale == 0.0f)) return EP_EINVAL;        // finite
+    if (!routing_ok(T, K) || E < 1 || E > EP_MAX_EXPERTS || K > E) return EP_EINVAL;
+    return EP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -594,6 +605,77 @@ int ep_topk_idx_narrow(const int64_t* topk_idx64, int64_t n, int32_t* topk_idx32
     if (n == 0) return EP_OK;
     if (!ptr_ok(topk_idx64, 8) || !ptr_ok(topk_idx32, 4)) return EP_EINVAL;
     return from_hip(ep::launch_idx_narrow(topk_idx64, n, topk_idx32, (hipStream_t)stream));
+}
+
+int ep_route(const void* logits, int dtype, int T, int E, int K, int score, const float* bias,
+             int renorm, float scale, int32_t* topk_idx, float* topk_w, void* stream)
+{
+    const int rc = route_args(dtype, T, E, K, score, renorm, scale);
+    if (rc != EP_OK) return rc;
+    if (bias != nullptr && (score != EP_SCORE_SIGMOID || !aligned(bias, 4))) return EP_EINVAL;
+    if (T == 0) return EP_OK;
+    if (!ptr_ok(logits, dtype == EP_DTYPE_BF16 ? 2 : 4) || !ptr_ok(topk_idx, 4) || !ptr_ok(topk_w, 4))
+        return EP_EINVAL;
+    return from_hip(ep::launch_route(logits, dtype == EP_DTYPE_BF16, T, E, K,
+                                     score == EP_SCORE_SIGMOID, bias, renorm != 0, scale, topk_idx,
+                                     topk_w, (hipStream_t)stream));
+}
+
+int ep_route_backward(const void* logits, int dtype, int T, int E, int K, int score, int renorm,
+                      float scale, const int32_t* topk_idx, const float* grad_topk_w,
+                      void* grad_logits, void* stream)
+{
+    const int rc = route_args(dtype, T, E, K, score, renorm, scale);
+    if (rc != EP_OK) return rc;
+    if (T == 0) return EP_OK;
+    const uintptr_t a = dtype == EP_DTYPE_BF16 ? 2 : 4;
+    if (!ptr_ok(logits, a) || !ptr_ok(topk_idx, 4) || !ptr_ok(grad_topk_w, 4) || !ptr_ok(grad_logits, a))
+        return EP_EINVAL;
+    return from_hip(ep::launch_route_backward(logits, dtype == EP_DTYPE_BF16, T, E, K,
+                                              score == EP_SCORE_SIGMOID, renorm != 0, scale,
+                                              topk_idx, grad_topk_w, grad_logits,
+                                              (hipStream_t)stream));
+}
+
+int ep_combine_backward(const uint16_t* grad_out, const uint16_t* expert_out,
+                        const int32_t* row_of_pair, const float* topk_w, int T, int H, int K,
+                        uint16_t* grad_expert_out, float* grad_topk_w, void* stream)
+{
+    if (!routing_ok(T, K) || H <= 0 || H % ep::kColsPerLane != 0) return EP_EINVAL;
+    if (T == 0) return EP_OK;
+    if (!ptr_ok(grad_out, 16) || !ptr_ok(expert_out, 16) || !ptr_ok(row_of_pair, 4) ||
+        !ptr_ok(topk_w, 4) || !ptr_ok(grad_expert_out, 16) || !ptr_ok(grad_topk_w, 4))
+        return EP_EINVAL;
+    return from_hip(ep::launch_combine_backward(grad_out, expert_out, row_of_pair, topk_w, T, H, K,
+                                                grad_expert_out, grad_topk_w, (hipStream_t)stream));
+}
+
+int ep_dispatch_backward(const uint16_t* grad_recv, const int32_t* row_of_pair, int T, int H, int K,
+                         uint16_t* grad_x, void* stream)
+{
+    // a token's rows summed with weight 1: the reduce level over K entries
+    static_assert(EP_MAX_TOPK <= EP_MAX_DEDUP_PARTITIONS, "K entries fit the reduce level");
+    return ep_combine_reduce(grad_recv, row_of_pair, T, H, K, grad_x, stream);
+}
+
+int ep_expert_w4(const void* x, const float* x_scales, int payload, int rows, int cols,
+                 const int32_t* expert_offset, int E, const uint8_t* w, const float* w_scales,
+                 int outs, int act, uint16_t* out, void* stream)
+{
+    if (payload != EP_PAYLOAD_FP8_E4M3FN && payload != EP_PAYLOAD_BF16) return EP_ENOTSUP;
+    if (act != EP_ACT_NONE && act != EP_ACT_SILU_MUL) return EP_EINVAL;
+    if (rows < 0 || E < 1 || E > EP_MAX_EXPERTS || cols <= 0 || cols % ep::kScaleBlock != 0 ||
+        outs <= 0 || outs % 8 != 0)
+        return EP_EINVAL;
+    if (!ep::expert_launch_ok(rows, outs, E)) return EP_EINVAL;
+    if (rows == 0) return EP_OK;
+    if (!ptr_ok(x, 16) || !ptr_ok(expert_offset, 4) || !ptr_ok(w, 16) || !ptr_ok(w_scales, 4) ||
+        !ptr_ok(out, 16))
+        return EP_EINVAL;
+    if (payload == EP_PAYLOAD_FP8_E4M3FN && !ptr_ok(x_scales, 4)) return EP_EINVAL;
+    return from_hip(ep::launch_expert(x, x_scales, payload == EP_PAYLOAD_FP8_E4M3FN, rows, cols,
+                                      expert_offset, E, w, w_scales, outs, act == EP_ACT_SILU_MUL,
+                                      out, (hipStream_t)stream));
 }
 
 int ep_graph_begin(void* stream)

@@ -99,4 +99,25 @@ hipError_t launch_e4m3fn_encode(const float* in, int64_t n, uint8_t* out,
 
 hipError_t launch_idx_narrow(const int64_t* in, int64_t n, int32_t* out, hipStream_t stream);
 
+hipError_t launch_route(const void* logits, bool bf16, int T, int E, int K, bool sigmoid_score,
+                        const float* bias, bool renorm, float scale, int32_t* topk_idx,
+                        float* topk_w, hipStream_t stream);
+
+hipError_t launch_route_backward(const void* logits, bool bf16, int T, int E, int K,
+                                 bool sigmoid_score, bool renorm, float scale,
+                                 const int32_t* topk_idx, const float* grad_w, void* grad_logits,
+                                 hipStream_t stream);
+
+hipError_t launch_combine_backward(const uint16_t* grad_out, const uint16_t* y,
+                                   const int32_t* row_of_pair, const float* topk_w, int T, int H,
+                                   int K, uint16_t* grad_y, float* grad_w, hipStream_t stream);
+
+// Whether launch_expert takes a batch of `rows` receive rows and `outs` outputs.
+bool expert_launch_ok(int rows, int outs, int E);
+
+hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int rows, int cols,
+                         const int32_t* expert_offset, int E, const uint8_t* w,
+                         const float* w_scales, int outs, bool silu, uint16_t* out,
+                         hipStream_t stream);
+
 }  // namespace ep

@@ -486,6 +486,126 @@ int ep_e4m3fn_encode(const float* in, int64_t n, uint8_t* out, void* stream);
  */
 int ep_topk_idx_narrow(const int64_t* topk_idx64, int64_t n, int32_t* topk_idx32, void* stream);
 
+/*
+ * Router: the K experts of each token and their weights, from its E logits --
+ * the topk_idx and topk_w that the layout, the dispatch and the combine take.
+ *   dtype     EP_DTYPE_F32 or EP_DTYPE_BF16, the type of logits [T, E].
+ *   score     EP_SCORE_SOFTMAX: p[t, e] = exp(l[t, e]) / sum over the row;
+ *             EP_SCORE_SIGMOID: p[t, e] = 1 / (1 + exp(-l[t, e])).
+ *   bias      fp32 [E] or NULL; with EP_SCORE_SIGMOID only.  It takes part in
+ *             the choice, not in the weights.
+ *   Choice: the K largest logits, or with a bias the K largest p + bias
+ *   (evaluated in 64 bits, so that neighbours do not swap), largest first,
+ *   ties to the lowest index (-0 equals +0).  A logit of -inf switches its
+ *   expert off (so does p + bias = -inf or NaN); when fewer than K can be
+ *   chosen, the entries left over get id -1, the masked entry of ep_layout,
+ *   and weight 0.
+ *   renorm    0: w[t, k] = scale * p of the k-th choice; 1: divided by the sum
+ *             of p over the row's choices.  (All weights 0 where that sum
+ *             underflows to 0.)
+ *   scale     a finite factor.
+ *   topk_idx  int32 [T, K] out.   topk_w  fp32 [T, K] out.
+ * Every value is computed in fp32.  A logit of +inf counts as the largest
+ * finite fp32; a NaN logit is not chosen and makes the weights of its row's
+ * choices NaN.
+ * Errors: EP_EINVAL for another dtype, score or renorm, a bias with softmax
+ * scores, a scale that is not finite, T < 0, K outside 1..16 or above E, E
+ * outside 1..1024, T*K >= 2^31, NULL or misaligned pointers (bf16 logits 2 B,
+ * the rest 4 B) when T > 0.
+ */
+#define EP_DTYPE_F32 0
+#define EP_DTYPE_BF16 1
+#define EP_SCORE_SOFTMAX 0
+#define EP_SCORE_SIGMOID 1
+
+int ep_route(const void* logits, int dtype, int T, int E, int K, int score, const float* bias,
+             int renorm, float scale, int32_t* topk_idx, float* topk_w, void* stream);
+
+/*
+ * Gradient of ep_route's weights with respect to the logits, for the choice
+ * topk_idx it made (the choice itself, and so the bias, has no gradient):
+ * grad_logits [T, E], in the logits' type, from grad_topk_w fp32 [T, K].
+ * With q the weights of ep_route before `scale` and dot = sum_k g[t,k] q[t,k]
+ *   softmax          scale * q_e * ([e chosen] g_e - dot)         for every e
+ *   softmax, renorm  scale * q_k * (g_k - dot)                    for the choices
+ *   sigmoid          scale * g_k * p_k * (1 - p_k)                for the choices
+ *   sigmoid, renorm  scale * q_k * (1 - p_k) * (g_k - dot)        for the choices
+ * and 0 elsewhere; computed in fp32 and rounded once.  Every element is
+ * written.  Entries whose id is negative or >= E take no part (their
+ * grad_topk_w is not used); the terms of an expert named twice are added.
+ * grad_logits must not overlap the inputs.
+ * Errors: those of ep_route.
+ */
+int ep_route_backward(const void* logits, int dtype, int T, int E, int K, int score, int renorm,
+                      float scale, const int32_t* topk_idx, const float* grad_topk_w,
+                      void* grad_logits, void* stream);
+
+/*
+ * Gradient of ep_combine: for every pair with r = row_of_pair[t*K+k] >= 0
+ *   grad_expert_out[r, c] = bf16_rne(topk_w[t,k] * grad_out[t, c])
+ *   grad_topk_w[t, k]     = sum_c grad_out[t, c] * expert_out[r, c]   (fp32)
+ * and grad_topk_w = 0 for a masked pair.  Rows of grad_expert_out that no pair
+ * names are left untouched.  The order of the sum is fixed.  It is also the
+ * gradient of the two dedup levels (ep_combine_partial, ep_combine_reduce)
+ * taken together: a partial row's gradient is its token's grad_out.
+ *   grad_out, expert_out, grad_expert_out  bf16 bits [T, H], [T*K, H],
+ *             [T*K, H], 16-byte aligned; grad_expert_out overlaps no input.
+ *   topk_w, grad_topk_w  fp32 [T, K].
+ * Errors: those of ep_combine.
+ */
+int ep_combine_backward(const uint16_t* grad_out, const uint16_t* expert_out,
+                        const int32_t* row_of_pair, const float* topk_w, int T, int H, int K,
+                        uint16_t* grad_expert_out, float* grad_topk_w, void* stream);
+
+/*
+ * Gradient of ep_dispatch: grad_x[t, c] = bf16_rne(acc), acc = 0.0f, then for
+ * k = 0..K-1 with r = row_of_pair[t*K+k] >= 0: acc = acc + grad_recv[r, c]
+ * (fp32).  A token with no row gets +0.  An fp8 payload is taken straight
+ * through: its rounding counts as the identity.  For the dedup dispatch call
+ * it with K = P and row_of_pair = tp_row.
+ *   grad_recv  bf16 bits [T*K, H] in the receive-row layout, all rows readable
+ *              (row 0 is read, unused, in place of masked entries);
+ *   grad_x     bf16 bits [T, H]; 16-byte aligned rows.
+ * Errors: EP_EINVAL as for ep_combine.
+ */
+int ep_dispatch_backward(const uint16_t* grad_recv, const int32_t* row_of_pair, int T, int H, int K,
+                         uint16_t* grad_x, void* stream);
+
+/*
+ * The experts' products with 4-bit weights, on receive rows in place: for the
+ * rows r of expert e (expert_offset[e] <= r < expert_offset[e+1])
+ *   acc[r, n] = sum over the 128-column blocks b, in ascending order, of
+ *               (sum over c in b of x[r, c] * v(w[e][n, c]))
+ *               * (w_scales[e][n, b] * x_scales[r, b])
+ * in fp32, v the value of a code, and
+ *   EP_ACT_NONE      out[r, n] = bf16_rne(acc[r, n]),  w has `outs` rows;
+ *   EP_ACT_SILU_MUL  out[r, n] = bf16_rne(g / (1 + exp(-g)) * u) with
+ *                    g = acc[r, n], u = acc[r, outs + n],  w has 2 * outs rows
+ *                    (the gate rows, then the up rows).
+ *   x         the receive rows [rows, cols], 16-byte aligned: e4m3fn bytes with
+ *             x_scales fp32 [rows, cols/128] (EP_PAYLOAD_FP8_E4M3FN, as
+ *             ep_dispatch writes them), or bf16 bits (EP_PAYLOAD_BF16;
+ *             x_scales is ignored and counts as 1).
+ *   expert_offset  int32 [E+1] from ep_layout, read on the device; rows past
+ *             expert_offset[E] are neither read nor written.
+ *   w         e2m1 codes, two per byte (even column in the low 4 bits):
+ *             uint8 [E, outs or 2*outs, cols/2], 16-byte aligned.  A code is
+ *             sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   w_scales  fp32 [E, outs or 2*outs, cols/128].
+ *   out       bf16 bits [rows, outs], 16-byte aligned, overlapping no input.
+ * cols % 128 == 0, outs % 8 == 0.
+ * Errors: EP_ENOTSUP for another payload; EP_EINVAL for another act, rows < 0,
+ * E outside 1..1024, cols or outs not positive or not divisible as above,
+ * NULL or misaligned pointers (x, w, out 16 B, the rest 4 B) when rows > 0,
+ * or rows / 16 + min(rows, E) >= 65536 (a grid limit).
+ */
+#define EP_ACT_NONE 0
+#define EP_ACT_SILU_MUL 1
+
+int ep_expert_w4(const void* x, const float* x_scales, int payload, int rows, int cols,
+                 const int32_t* expert_offset, int E, const uint8_t* w, const float* w_scales,
+                 int outs, int act, uint16_t* out, void* stream);
+
 /* Message for a return code; static storage. */
 const char* ep_strerror(int code);
 /* hipError_t of the last failed launch in the calling thread (0 if none). */
