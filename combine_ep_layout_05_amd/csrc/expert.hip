@@ -36,38 +36,31 @@ constexpr int kExpertWaves = 4;
 
 // Row tile `idx` of the batch: its expert, first row and row count, from the
 // expert offsets (clamped to the rows there are).  False past the last tile.
-// Called by whole waves; the result is wave-uniform.
+// Called by whole waves; the result is wave-uniform.  64 experts a round, one
+// per lane: tiles before each by a DPP scan, the expert that holds `idx` by a
+// ballot.
 template <int kRows>
 __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ off, int E, int rows, int idx,
                                           int lane, int& expert, int& row0, int& count)
 {
-    const int per = (E + kWave - 1) / kWave;
-    const int e0 = lane * per;
-    int tiles = 0;
-    for (int j = 0; j < per; ++j) {
-        const int e = e0 + j;
-        if (e >= E) break;
-        const int a = min(max(off[e], 0), rows), b = min(max(off[e + 1], a), rows);
-        tiles += (b - a + kRows - 1) / kRows;
-    }
-    const int incl = wave_inclusive_scan(tiles);
-    const uint64_t past = __ballot(incl > idx);
-    if (!past) return false;
-    const int win = __builtin_ctzll(past);
-    int left = idx - read_lane(incl - tiles, win);
-    const int first = win * per;
-    for (int j = 0; j < per; ++j) {
-        const int e = first + j;
-        if (e >= E) break;
-        const int a = min(max(off[e], 0), rows), b = min(max(off[e + 1], a), rows);
-        const int n = (b - a + kRows - 1) / kRows;
-        if (left < n) {
-            expert = e;
-            row0 = a + left * kRows;
-            count = min(kRows, b - row0);
+    int left = idx;
+    for (int e0 = 0; e0 < E; e0 += kWave) {
+        const int e = min(e0 + lane, E - 1);
+        int a = off[e], b = off[e + 1];
+        a = min(max(a, 0), rows);
+        b = min(max(b, a), rows);
+        const int tiles = e0 + lane < E ? (b - a + kRows - 1) / kRows : 0;
+        const int incl = wave_inclusive_scan(tiles);
+        const uint64_t past = __ballot(incl > left);
+        if (past) {
+            const int win = __builtin_ctzll(past);
+            left -= read_lane(incl - tiles, win);
+            expert = e0 + win;
+            row0 = read_lane(a, win) + left * kRows;
+            count = min(kRows, read_lane(b, win) - row0);
             return true;
         }
-        left -= n;
+        left -= read_lane(incl, kWave - 1);
     }
     return false;
 }
@@ -92,9 +85,8 @@ __device__ __forceinline__ v4f block_product(v4i w, v8i x)
 {
     const v8i a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
     const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    // cbsz 4: A is e2m1; blgp 0: B is e4m3; e8m0 scales of 127: factors of 1
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, x, zero, 4, 0, 0, 0x7F7F7F7F, 0,
-                                                            0x7F7F7F7F);
+    // cbsz 4: A is e2m1; blgp 0: B is e4m3; no block scales (the unscaled form)
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, x, zero, 4, 0, 0, 0, 0, 0);
 }
 
 __device__ __forceinline__ v4f block_product(v4i w, const v4i (&x)[4])
@@ -173,12 +165,207 @@ __global__ __launch_bounds__(kExpertWaves * kWave) void expert_kernel(
     }
 }
 
+// Large batches: a workgroup computes up to kTileRows rows x 4 * kWaveCols
+// weight rows.  Every wave has its own weight rows, loaded straight into
+// registers (no other wave needs them), and all the rows: those go through
+// LDS, one 128-column block at a time, double buffered, loaded one block
+// ahead.  Row groups of 16 past the last row are skipped.
+constexpr int kWaveCols = 64;                    // weight rows per wave: 4 operand tiles
+constexpr int kColTiles = kWaveCols / kTile;
+
+template <bool kFp8> struct TileShape {
+    static constexpr int kRows = 64;                         // rows per workgroup
+    static constexpr int kRowTiles = kRows / kTile;
+    static constexpr int kBlockBytes = kScaleBlock * (kFp8 ? 1 : 2);
+    static constexpr int kPieces = kRows * kBlockBytes / 1024 / kExpertWaves;   // 1 KB loads per wave
+};
+
+template <bool kFp8, bool kSilu>
+__global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
+    const uint8_t* __restrict__ x, const float* __restrict__ xs, int rows, int cols,
+    const int32_t* __restrict__ off, int E, const uint8_t* __restrict__ w,
+    const float* __restrict__ ws, int outs, uint16_t* __restrict__ out, int n_groups)
+{
+    using S = TileShape<kFp8>;
+    __shared__ __attribute__((aligned(16))) uint8_t s_x[2][S::kRows * S::kBlockBytes];
+    __shared__ float s_xs[2][kFp8 ? S::kRows : 1];
+    __shared__ __attribute__((aligned(16))) float s_ws[2][kExpertWaves][kWaveCols];
+    const int lane = threadIdx.x % kWave, m = lane % kTile, q = lane / kTile;
+    const int wave = wave_uniform(threadIdx.x / kWave);
+    // the column groups of one row tile on one XCD (they share its rows)
+    const int slot = blockIdx.x / kXcds;
+    const int tile = (slot / n_groups) * kXcds + blockIdx.x % kXcds;
+    constexpr int kOuts = kSilu ? kWaveCols / 2 : kWaveCols;   // outputs per wave
+    const int n0 = ((slot % n_groups) * kExpertWaves + wave) * kOuts;
+    int expert, row0, count;
+    if (!find_tile<S::kRows>(off, E, rows, tile, lane, expert, row0, count)) return;
+    const int live = (count + kTile - 1) / kTile;
+    const int blocks = cols / kScaleBlock;
+    const int64_t wrows = kSilu ? 2 * (int64_t)outs : outs;
+
+    // operand tile j: weight rows n0 + 16 j (silu: two of the gate, then the two of the up rows)
+    // (a uniform base and a 32-bit offset per lane, which stays below 16 rows)
+    const uint8_t* wp[kColTiles];
+    int wo[kColTiles];
+#pragma unroll
+    for (int j = 0; j < kColTiles; ++j) {
+        const int h = kSilu ? j / 2 : 0, t = kSilu ? j % 2 : j;
+        const int n = min(n0 + t * kTile, outs - 1);
+        wp[j] = w + (expert * wrows + (int64_t)h * outs + n) * (cols / 2);
+        wo[j] = min(m, outs - 1 - n) * (cols / 2) + q * 16;
+    }
+    // lane i of a wave stages the scale of weight row (i / 16, i % 16) of its tiles
+    const float* wsp;
+    {
+        const int h = kSilu ? q / 2 : 0, t = kSilu ? q % 2 : q;
+        wsp = ws + (expert * wrows + (int64_t)h * outs + min(n0 + t * kTile + m, outs - 1)) * blocks;
+    }
+    // a wave stages row tile `wave`; fp8: piece p is half p of its operand, in
+    // operand order; bf16: rows 4 p .. 4 p + 3, 16-byte pieces of row r at r ^ piece
+    const uint8_t* const xp = x + (int64_t)row0 * cols * (kFp8 ? 1 : 2);
+    int xo[S::kPieces];
+    int xdst[S::kPieces];
+    const bool xlive = wave < live;
+#pragma unroll
+    for (int p = 0; p < S::kPieces; ++p) {
+        if constexpr (kFp8) {
+            xo[p] = min(wave * kTile + m, count - 1) * cols + p * 64 + q * 16;
+            xdst[p] = (wave * 2 + p) * 1024 + lane * 16;
+        } else {
+            const int r = wave * kTile + p * 4 + q;
+            xo[p] = min(r, count - 1) * cols * 2 + m * 16;
+            xdst[p] = r * 256 + ((m ^ (r % kTile)) * 16);
+        }
+    }
+    const int xs_row = threadIdx.x;                 // fp8: thread i stages the scale of row i
+    const float* const xsp = kFp8 ? xs + (int64_t)(row0 + min(xs_row, count - 1)) * blocks : nullptr;
+
+    v4i xr[S::kPieces], wr[kColTiles];
+    float xsr = 0.0f, wsr;
+    auto load = [&](int b) {
+#pragma unroll
+        for (int p = 0; p < S::kPieces; ++p)
+            if (xlive) xr[p] = *(const v4i*)(xp + (int64_t)b * S::kBlockBytes + (uint32_t)xo[p]);
+        if constexpr (kFp8) if (xs_row < S::kRows) xsr = xsp[b];
+        wsr = wsp[b];
+    };
+    auto load_w = [&](int b) {
+#pragma unroll
+        for (int j = 0; j < kColTiles; ++j) wr[j] = *(const v4i*)(wp[j] + (int64_t)b * 64 + (uint32_t)wo[j]);
+    };
+    v4f acc[S::kRowTiles][kColTiles];
+#pragma unroll
+    for (int t = 0; t < S::kRowTiles; ++t)
+#pragma unroll
+        for (int j = 0; j < kColTiles; ++j) acc[t][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+
+    load(0);
+    load_w(0);
+    for (int b = 0; b < blocks; ++b) {
+        const int buf = b & 1;
+#pragma unroll
+        for (int p = 0; p < S::kPieces; ++p)
+            if (xlive) *(v4i*)(s_x[buf] + xdst[p]) = xr[p];
+        if constexpr (kFp8) if (xs_row < S::kRows) s_xs[buf][xs_row] = xsr;
+        s_ws[buf][wave][lane] = wsr;
+        lds_barrier();
+        v4i wc[kColTiles];
+#pragma unroll
+        for (int j = 0; j < kColTiles; ++j) wc[j] = wr[j];
+        if (b + 1 < blocks) { load(b + 1); load_w(b + 1); }
+        v4f sw[kColTiles];
+#pragma unroll
+        for (int j = 0; j < kColTiles; ++j) sw[j] = *(const v4f*)&s_ws[buf][wave][j * kTile + q * 4];
+        if constexpr (kFp8) {
+#pragma unroll
+            for (int t = 0; t < S::kRowTiles; ++t) {
+                if (t >= live) break;
+                const v4i lo = *(const v4i*)(s_x[buf] + t * 2048 + lane * 16);
+                const v4i hi = *(const v4i*)(s_x[buf] + t * 2048 + 1024 + lane * 16);
+                const v8i xb = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                const float f = s_xs[buf][t * kTile + m];
+                v4f d[kColTiles];
+#pragma unroll
+                for (int j = 0; j < kColTiles; ++j) d[j] = block_product(wc[j], xb);
+#pragma unroll
+                for (int j = 0; j < kColTiles; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[t][j][i] = __builtin_fmaf(d[j][i], sw[j][i] * f, acc[t][j][i]);
+            }
+        } else {
+            v8bf wb[kColTiles][4];
+#pragma unroll
+            for (int j = 0; j < kColTiles; ++j)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) wb[j][s] = bf16x8_of_codes((uint32_t)wc[j][s]);
+#pragma unroll
+            for (int t = 0; t < S::kRowTiles; ++t) {
+                if (t >= live) break;
+                v8bf xb[4];
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    xb[s] = *(const v8bf*)(s_x[buf] + (t * kTile + m) * 256 + (((q * 4 + s) ^ m) * 16));
+#pragma unroll
+                for (int j = 0; j < kColTiles; ++j) {
+                    v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][s], xb[s], d, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[t][j][i] = __builtin_fmaf(d[i], sw[j][i], acc[t][j][i]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < S::kRowTiles; ++t) {
+        const int r = t * kTile + m;
+        if (r >= count) continue;
+        uint16_t* const orow = out + (int64_t)(row0 + r) * outs;
+#pragma unroll
+        for (int j = 0; j < (kSilu ? kColTiles / 2 : kColTiles); ++j) {
+            const int n = n0 + j * kTile + q * 4;
+            if (n >= outs) continue;
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = kSilu ? silu_mul(acc[t][j][i], acc[t][j + kColTiles / 2][i]) : acc[t][j][i];
+            store8<false>(orow + n, make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])));
+        }
+    }
+}
+
 }  // namespace
 
-bool expert_launch_ok(int rows, int outs, int E)
+namespace {
+
+// Row tiles of the given height a batch can have: at most one partly filled
+// tile per expert that has rows.
+int64_t max_tiles(int rows, int E, int height)
 {
-    const int64_t tiles = (int64_t)rows / kTile + (rows < E ? rows : E);
-    return tiles < 65536 && (int64_t)outs + kTile * kExpertWaves < ((int64_t)1 << 31);
+    return (int64_t)rows / height + (rows < E ? rows : E);
+}
+
+// Few rows per expert: the kernel that streams the weights; more: the tiles.
+bool expert_large(int rows, int E) { return rows > 8 * (int64_t)E; }
+
+int64_t tile_blocks(bool fp8, bool silu, int rows, int outs, int E)
+{
+    const int per = kExpertWaves * (silu ? kWaveCols / 2 : kWaveCols);
+    const int64_t groups = ((int64_t)outs + per - 1) / per;
+    const int64_t tiles = max_tiles(rows, E, fp8 ? TileShape<true>::kRows : TileShape<false>::kRows);
+    return (tiles + kXcds - 1) / kXcds * kXcds * groups;
+}
+
+}  // namespace
+
+bool expert_launch_ok(bool fp8, bool silu, int rows, int outs, int E)
+{
+    if ((int64_t)outs + kTile * kExpertWaves >= ((int64_t)1 << 30)) return false;
+    if (expert_large(rows, E)) return tile_blocks(fp8, silu, rows, outs, E) < ((int64_t)1 << 31);
+    return max_tiles(rows, E, kTile) < 65536;
 }
 
 hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int rows, int cols,
@@ -186,12 +373,24 @@ hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int row
                          const float* w_scales, int outs, bool silu, uint16_t* out,
                          hipStream_t stream)
 {
-    // at most one partly filled tile per expert that has rows
-    const int tiles = rows / kTile + (rows < E ? rows : E);
-    const dim3 grid((unsigned)((outs + kTile * kExpertWaves - 1) / (kTile * kExpertWaves)), (unsigned)tiles);
+    const dim3 block(kExpertWaves * kWave);
+    if (expert_large(rows, E)) {
+        const int per = kExpertWaves * (silu ? kWaveCols / 2 : kWaveCols);
+        const int groups = (outs + per - 1) / per;
+        const dim3 grid((unsigned)tile_blocks(fp8, silu, rows, outs, E));
+        auto go = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid, block, 0, stream, (const uint8_t*)x, x_scales, rows,
+                               cols, expert_offset, E, w, w_scales, outs, out, groups);
+        };
+        if (fp8) silu ? go(expert_tile_kernel<true, true>) : go(expert_tile_kernel<true, false>);
+        else silu ? go(expert_tile_kernel<false, true>) : go(expert_tile_kernel<false, false>);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)((outs + kTile * kExpertWaves - 1) / (kTile * kExpertWaves)),
+                    (unsigned)max_tiles(rows, E, kTile));
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(kExpertWaves * kWave), 0, stream, (const uint8_t*)x,
-                           x_scales, rows, cols, expert_offset, E, w, w_scales, outs, out);
+        hipLaunchKernelGGL(kernel, grid, block, 0, stream, (const uint8_t*)x, x_scales, rows, cols,
+                           expert_offset, E, w, w_scales, outs, out);
     };
     if (fp8) silu ? go(expert_kernel<true, true>) : go(expert_kernel<true, false>);
     else silu ? go(expert_kernel<false, true>) : go(expert_kernel<false, false>);
