@@ -112,8 +112,9 @@ hipError_t launch_combine_backward(const uint16_t* grad_out, const uint16_t* y,
                                    const int32_t* row_of_pair, const float* topk_w, int T, int H,
                                    int K, uint16_t* grad_y, float* grad_w, hipStream_t stream);
 
-// Whether launch_expert takes a batch of `rows` receive rows and `outs` outputs.
-bool expert_launch_ok(bool fp8, bool silu, int rows, int outs, int E);
+// Whether launch_expert takes a batch of `rows` receive rows of `cols` columns
+// and `outs` outputs.
+bool expert_launch_ok(bool fp8, bool silu, int rows, int cols, int outs, int E);
 
 hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int rows, int cols,
                          const int32_t* expert_offset, int E, const uint8_t* w,

@@ -18,6 +18,8 @@
 // 64 + q*16 .. +15 in lane l (16 bytes each; read off the instruction with
 // one-hot operands).  bf16 rows: the columns of the codes, 8 per instruction
 // (16 bytes each).
+#include <algorithm>
+
 #include "ep_device.h"
 #include "ep_launch.h"
 #include "ep_numerics.h"
@@ -33,6 +35,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kTile = 16;
 constexpr int kExpertWaves = 4;
+constexpr int kMaxExpertCols = 1 << 24;      // 64 rows of bf16 within 32-bit offsets
 
 // Row tile `idx` of the batch: its expert, first row and row count, from the
 // expert offsets (clamped to the rows there are).  False past the last tile.
@@ -101,67 +104,145 @@ __device__ __forceinline__ v4f block_product(v4i w, const v4i (&x)[4])
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// One wave per tile of 16 outputs x 16 rows (with kSilu: 16 gate rows and the
-// 16 up rows that belong to them).
+// Few rows per expert: the weights are read once and bound the time, so the
+// work is split for loads in flight.  A workgroup of 8 waves takes 16 rows of
+// one expert and a share of the weight rows, 64 (silu: 32 + 32) at a time; its
+// waves split the columns, wave i taking blocks i, i + 8, ..., and always have
+// the next block's codes and rows in flight, across the groups of 64 too.  The
+// waves' sums are joined through LDS in wave order.  The scales of a group are
+// one contiguous piece of memory; they are copied to LDS transposed, a window
+// of at most 64 blocks at a time.
+constexpr int kStreamWaves = 8;
+constexpr int kGroupRows = 64;                    // weight rows per group: 4 operand tiles
+constexpr int kGroupTiles = kGroupRows / kTile;
+constexpr int kWindow = 64;                       // blocks whose scales are in LDS
+constexpr int kScaleRows = kGroupRows + kTile;    // weight rows, then fp8 rows
+constexpr int kScalePitch = kScaleRows + 4;
+
 template <bool kFp8, bool kSilu>
-__global__ __launch_bounds__(kExpertWaves * kWave) void expert_kernel(
+__global__ __launch_bounds__(kStreamWaves * kWave, 4) void expert_stream_kernel(
     const uint8_t* __restrict__ x, const float* __restrict__ xs, int rows, int cols,
     const int32_t* __restrict__ off, int E, const uint8_t* __restrict__ w,
-    const float* __restrict__ ws, int outs, uint16_t* __restrict__ out)
+    const float* __restrict__ ws, int outs, uint16_t* __restrict__ out, int n_groups, int n_split)
 {
+    __shared__ __attribute__((aligned(16))) float s_scale[2][kWindow * kScalePitch];
+    __shared__ v4f s_part[kStreamWaves][kGroupTiles][kWave];
     const int lane = threadIdx.x % kWave, m = lane % kTile, q = lane / kTile;
-    const int n0 = (blockIdx.x * kExpertWaves + wave_uniform(threadIdx.x / kWave)) * kTile;
-    if (n0 >= outs) return;
+    const int wave = wave_uniform(threadIdx.x / kWave);
+    constexpr int kOuts = kSilu ? kGroupRows / 2 : kGroupRows;      // outputs per group
     int expert, row0, count;
-    if (!find_tile<kTile>(off, E, rows, blockIdx.y, lane, expert, row0, count)) return;
+    if (!find_tile<kTile>(off, E, rows, blockIdx.x / n_split, lane, expert, row0, count)) return;
+    const int g0 = blockIdx.x % n_split;
     const int blocks = cols / kScaleBlock;
-    const int64_t wrows = kSilu ? 2 * (int64_t)outs : outs;
+    const int windows = (blocks + kWindow - 1) / kWindow;
+    const int64_t wrow0 = expert * (kSilu ? 2 * (int64_t)outs : (int64_t)outs);
     // lanes past the last row or output read a valid one; what they compute is not stored
-    const int64_t row = row0 + min(m, count - 1);
-    const uint8_t* const xr = x + row * cols * (kFp8 ? 1 : 2) + q * (kFp8 ? 16 : 64);
-    const float* const xsr = kFp8 ? xs + row * blocks : nullptr;
-    const int n_load = min(n0 + m, outs - 1);
-    const uint8_t* wr[2];
-    const float* sr[2];
+    const uint8_t* const xb = x + (int64_t)row0 * cols * (kFp8 ? 1 : 2);
+    const uint32_t xo = (uint32_t)min(m, count - 1) * cols * (kFp8 ? 1 : 2) + q * (kFp8 ? 16 : 64);
+
+    constexpr int kXRegs = kFp8 ? 2 : 4;
+    struct Step { v4i w[kGroupTiles]; v4i x[kXRegs]; };
+    // weight row j * 16 + m of group g (silu: tiles 0, 1 gate, 2, 3 up)
+    auto weight_row = [&](int g, int r) {
+        const int h = kSilu ? r / kOuts : 0;
+        return wrow0 + (int64_t)h * outs + min(g * kOuts + (kSilu ? r % kOuts : r), outs - 1);
+    };
+    auto load = [&](Step& s, int g, int b) {
 #pragma unroll
-    for (int h = 0; h < (kSilu ? 2 : 1); ++h) {
-        const int64_t base = expert * wrows + (int64_t)h * outs;
-        wr[h] = w + (base + n_load) * (cols / 2) + q * 16;
-        sr[h] = ws + (base + n0) * blocks;
-    }
-    int ns[4];
+        for (int j = 0; j < kGroupTiles; ++j)
+            s.w[j] = *(const v4i*)(w + weight_row(g, j * kTile + m) * (cols / 2) + b * 64 + q * 16);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ns[i] = (min(n0 + q * 4 + i, outs - 1) - n0) * blocks;
-    v4f acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    for (int b = 0; b < blocks; ++b) {
-        v8i x8;
-        v4i x16[4];
-        float f = 1.0f;
-        if constexpr (kFp8) {
-            const v4i lo = *(const v4i*)(xr + b * 128), hi = *(const v4i*)(xr + b * 128 + 64);
-            x8 = (v8i){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            f = xsr[b];
-        } else {
+        for (int i = 0; i < kXRegs; ++i)
+            s.x[i] = *(const v4i*)(xb + xo + b * (kFp8 ? 128 : 256) + i * (kFp8 ? 64 : 16));
+    };
+    // the scales of 10 rows per wave, lane = block of the window
+    constexpr int kMine = kFp8 ? kScaleRows / kStreamWaves : kGroupRows / kStreamWaves;
+    float sc[kMine];
+    auto load_scales = [&](int g, int win) {
+        const int b = win * kWindow + lane;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x16[i] = *(const v4i*)(xr + b * 256 + i * 16);
+        for (int i = 0; i < kMine; ++i) {
+            const int r = i * kStreamWaves + wave;
+            const float* p = r < kGroupRows ? ws + weight_row(g, r) * blocks
+                                            : xs + (int64_t)(row0 + min(r - kGroupRows, count - 1)) * blocks;
+            sc[i] = b < blocks ? p[b] : 0.0f;
         }
+    };
+    auto store_scales = [&](int buf) {
 #pragma unroll
-        for (int h = 0; h < (kSilu ? 2 : 1); ++h) {
-            const v4i wc = *(const v4i*)(wr[h] + b * 64);
-            v4f d;
-            if constexpr (kFp8) d = block_product(wc, x8);
-            else d = block_product(wc, x16);
+        for (int i = 0; i < kMine; ++i) s_scale[buf][lane * kScalePitch + i * kStreamWaves + wave] = sc[i];
+    };
+
+    if (g0 >= n_groups) return;
+    Step cur, next;
+    load_scales(g0, 0);
+    if (wave < blocks) load(cur, g0, wave);
+    store_scales(0);
+    __syncthreads();
+    int buf = 0;
+    for (int g = g0; g < n_groups; g += n_split) {
+        v4f acc[kGroupTiles];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[h][i] = __builtin_fmaf(d[i], sr[h][ns[i] + b] * f, acc[h][i]);
+        for (int j = 0; j < kGroupTiles; ++j) acc[j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+        for (int win = 0; win < windows; ++win) {
+            const bool last = win + 1 == windows;
+            const int g_next = last ? g + n_split : g;
+            const bool more = g_next < n_groups;
+            if (more) load_scales(g_next, last ? 0 : win + 1);
+            const int end = min(blocks, (win + 1) * kWindow);
+            for (int b = win * kWindow + wave; b < end; b += kStreamWaves) {
+                // the block after this one, in this window, the next or the next group
+                const int bn = b + kStreamWaves;
+                if (bn < blocks) load(next, g, bn);
+                else if (g + n_split < n_groups) load(next, g + n_split, wave);
+                const float* const sb = s_scale[buf] + (b - win * kWindow) * kScalePitch;
+                const float f = kFp8 ? sb[kGroupRows + m] : 1.0f;
+#pragma unroll
+                for (int j = 0; j < kGroupTiles; ++j) {
+                    const v4f sw = *(const v4f*)(sb + j * kTile + q * 4);
+                    v4f d;
+                    if constexpr (kFp8) {
+                        const v8i xv = {cur.x[0][0], cur.x[0][1], cur.x[0][2], cur.x[0][3],
+                                        cur.x[1][0], cur.x[1][1], cur.x[1][2], cur.x[1][3]};
+                        d = block_product(cur.w[j], xv);
+                    } else {
+                        d = block_product(cur.w[j], cur.x);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j][i] = __builtin_fmaf(d[i], sw[i] * f, acc[j][i]);
+                }
+                cur = next;
+            }
+            buf ^= 1;
+            if (more) store_scales(buf);
+            if (last)
+#pragma unroll
+                for (int j = 0; j < kGroupTiles; ++j) s_part[wave][j][lane] = acc[j];
+            lds_barrier();
         }
-    }
-    const int n = n0 + q * 4;
-    if (m < count && n < outs) {
-        float v[4];
+        // two neighbouring outputs per thread: lane's quarter `half` of operand tile j
+        const int idx = threadIdx.x / 2, half = threadIdx.x % 2;
+        const int j = idx / kWave, ln = idx % kWave;
+        if (j < kOuts / kTile) {
+            float v[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = kSilu ? silu_mul(acc[0][i], acc[1][i]) : acc[0][i];
-        const uint2 o = make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]));
-        store8<false>(out + row * outs + n, o);
+            for (int i = 0; i < kStreamWaves; ++i) {
+                const float* const p = (const float*)&s_part[i][j][ln] + half * 2;
+                v[0] += p[0];
+                v[1] += p[1];
+                if constexpr (kSilu) {
+                    const float* const pu = (const float*)&s_part[i][j + kOuts / kTile][ln] + half * 2;
+                    u[0] += pu[0];
+                    u[1] += pu[1];
+                }
+            }
+            const int r = ln % kTile, n = g * kOuts + j * kTile + (ln / kTile) * 4 + half * 2;
+            if (r < count && n < outs) {
+                if constexpr (kSilu) { v[0] = silu_mul(v[0], u[0]); v[1] = silu_mul(v[1], u[1]); }
+                *(uint32_t*)(out + (int64_t)(row0 + r) * outs + n) = pack2_bf16(v[0], v[1]);
+            }
+        }
+        lds_barrier();
     }
 }
 
@@ -348,6 +429,8 @@ int64_t max_tiles(int rows, int E, int height)
     return (int64_t)rows / height + (rows < E ? rows : E);
 }
 
+constexpr int64_t kStreamBlocks = 4096;
+
 // Few rows per expert: the kernel that streams the weights; more: the tiles.
 bool expert_large(int rows, int E) { return rows > 8 * (int64_t)E; }
 
@@ -361,11 +444,12 @@ int64_t tile_blocks(bool fp8, bool silu, int rows, int outs, int E)
 
 }  // namespace
 
-bool expert_launch_ok(bool fp8, bool silu, int rows, int outs, int E)
+bool expert_launch_ok(bool fp8, bool silu, int rows, int cols, int outs, int E)
 {
-    if ((int64_t)outs + kTile * kExpertWaves >= ((int64_t)1 << 30)) return false;
-    if (expert_large(rows, E)) return tile_blocks(fp8, silu, rows, outs, E) < ((int64_t)1 << 31);
-    return max_tiles(rows, E, kTile) < 65536;
+    // offsets within a tile are 32-bit; a grid dimension holds fewer than 2^32 threads
+    if (cols > kMaxExpertCols || outs > (1 << 29)) return false;
+    if (!expert_large(rows, E)) return true;       // at most kStreamBlocks + max_tiles workgroups
+    return tile_blocks(fp8, silu, rows, outs, E) * kExpertWaves * kWave < ((int64_t)1 << 32);
 }
 
 hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int rows, int cols,
@@ -386,14 +470,19 @@ hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int row
         else silu ? go(expert_tile_kernel<false, true>) : go(expert_tile_kernel<false, false>);
         return hipGetLastError();
     }
-    const dim3 grid((unsigned)((outs + kTile * kExpertWaves - 1) / (kTile * kExpertWaves)),
-                    (unsigned)max_tiles(rows, E, kTile));
+    const int per = silu ? kGroupRows / 2 : kGroupRows;
+    const int groups = (outs + per - 1) / per;
+    const int64_t tiles = max_tiles(rows, E, kTile);
+    // about kStreamBlocks workgroups: several rounds of the 512 that run at once
+    const int split = (int)std::min<int64_t>(groups, (kStreamBlocks + tiles - 1) / tiles);
+    const dim3 grid((unsigned)(tiles * split));
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, block, 0, stream, (const uint8_t*)x, x_scales, rows, cols,
-                           expert_offset, E, w, w_scales, outs, out);
+        hipLaunchKernelGGL(kernel, grid, dim3(kStreamWaves * kWave), 0, stream, (const uint8_t*)x,
+                           x_scales, rows, cols, expert_offset, E, w, w_scales, outs, out, groups,
+                           split);
     };
-    if (fp8) silu ? go(expert_kernel<true, true>) : go(expert_kernel<true, false>);
-    else silu ? go(expert_kernel<false, true>) : go(expert_kernel<false, false>);
+    if (fp8) silu ? go(expert_stream_kernel<true, true>) : go(expert_stream_kernel<true, false>);
+    else silu ? go(expert_stream_kernel<false, true>) : go(expert_stream_kernel<false, false>);
     return hipGetLastError();
 }
 

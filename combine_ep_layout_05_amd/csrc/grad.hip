@@ -20,6 +20,7 @@ namespace ep {
 namespace {
 
 constexpr int kGradWaves = 4;
+constexpr int kMaxGradBlocks = 1 << 20;
 
 __device__ __forceinline__ float wave_sum_f(float v)
 {
@@ -50,13 +51,17 @@ __global__ __launch_bounds__(kGradWaves * kWave) void combine_backward_kernel(
     const int32_t* __restrict__ row_of_pair, const float* __restrict__ topk_w, int n_pairs, int H,
     int K, uint16_t* __restrict__ grad_y, float* __restrict__ grad_w)
 {
-    const int pair = xcd_block(blockIdx.x, gridDim.x);
+  __shared__ float part[kGradWaves];
+  for (int64_t first = 0; first < n_pairs; first += gridDim.x) {
+    const int in_grid = (int)min((int64_t)gridDim.x, n_pairs - first);
+    if ((int)blockIdx.x >= in_grid) return;
+    const int pair = (int)first + xcd_block(blockIdx.x, in_grid);
     const int t = pair / K;
     const int row = row_of_pair[pair];
     const float w = topk_w[pair];
     if (row < 0 || row >= n_pairs) {
         if (threadIdx.x == 0) grad_w[pair] = 0.0f;
-        return;
+        continue;
     }
     const uint16_t* const g = grad_out + (int64_t)t * H;
     const uint16_t* const yr = y + (int64_t)row * H;
@@ -67,7 +72,6 @@ __global__ __launch_bounds__(kGradWaves * kWave) void combine_backward_kernel(
         acc += grad_step(load16<false>(g + c), load16<kStream>(yr + c), w, ov);
         store16<kStream>(o + c, ov);
     }
-    __shared__ float part[kGradWaves];
     acc = wave_sum_f(acc);
     if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = acc;
     __syncthreads();
@@ -77,6 +81,8 @@ __global__ __launch_bounds__(kGradWaves * kWave) void combine_backward_kernel(
         for (int i = 0; i < kGradWaves; ++i) s += part[i];
         grad_w[pair] = s;
     }
+    __syncthreads();                              // part is used again
+  }
 }
 
 }  // namespace
@@ -86,7 +92,7 @@ hipError_t launch_combine_backward(const uint16_t* grad_out, const uint16_t* y,
                                    int K, uint16_t* grad_y, float* grad_w, hipStream_t stream)
 {
     const int n = T * K;
-    const dim3 grid((unsigned)n), block(kGradWaves * kWave);
+    const dim3 grid((unsigned)(n < kMaxGradBlocks ? n : kMaxGradBlocks)), block(kGradWaves * kWave);
     if ((int64_t)n * H * 2 >= kStreamMinBytes)
         hipLaunchKernelGGL(combine_backward_kernel<true>, grid, block, 0, stream, grad_out, y,
                            row_of_pair, topk_w, n, H, K, grad_y, grad_w);

@@ -100,15 +100,15 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(
 {
     using Key = typename std::conditional<kBias, uint64_t, uint32_t>::type;
     const int lane = threadIdx.x % kWave;
-    const int t = blockIdx.x * kRouteWaves + wave_uniform(threadIdx.x / kWave);
-    if (t >= T) return;
+    for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave_uniform(threadIdx.x / kWave); t < T;
+         t += (int64_t)gridDim.x * kRouteWaves) {
     float l[kPer];
     Key key[kPer];
     bool nan = false;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const int e = j * kWave + lane;
-        l[j] = e < E ? load_logit<kBf16>(logits, (int64_t)t * E + e) : -__builtin_inff();
+        l[j] = e < E ? load_logit<kBf16>(logits, t * E + e) : -__builtin_inff();
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -169,8 +169,9 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_kernel(
     if (lane < K) {
         float v = 0.0f;
         if (my_id >= 0) v = row_nan ? __builtin_nanf("") : scale * (total > 0.0f ? w / total : 0.0f);
-        topk_idx[(int64_t)t * K + lane] = my_id;
-        topk_w[(int64_t)t * K + lane] = v;
+        topk_idx[t * K + lane] = my_id;
+        topk_w[t * K + lane] = v;
+    }
     }
 }
 
@@ -189,13 +190,13 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(
 {
     constexpr bool kFull = !kSigmoid && !kRenorm;          // every expert of the row is involved
     const int lane = threadIdx.x % kWave;
-    const int t = blockIdx.x * kRouteWaves + wave_uniform(threadIdx.x / kWave);
-    if (t >= T) return;
+    for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave_uniform(threadIdx.x / kWave); t < T;
+         t += (int64_t)gridDim.x * kRouteWaves) {
     const int kl = lane < K ? lane : 0;
-    int id = topk_idx[(int64_t)t * K + kl];
-    float g = grad_w[(int64_t)t * K + kl];
+    int id = topk_idx[t * K + kl];
+    float g = grad_w[t * K + kl];
     if (lane >= K || id < 0 || id >= E) { id = -1; g = 0.0f; }
-    const float lk = id >= 0 ? load_logit<kBf16>(logits, (int64_t)t * E + id) : -__builtin_inff();
+    const float lk = id >= 0 ? load_logit<kBf16>(logits, t * E + id) : -__builtin_inff();
 
     float out[kPer];
 #pragma unroll
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int e = j * kWave + lane;
-            l[j] = e < E ? load_logit<kBf16>(logits, (int64_t)t * E + e) : -__builtin_inff();
+            l[j] = e < E ? load_logit<kBf16>(logits, t * E + e) : -__builtin_inff();
             mk = __builtin_elementwise_max(mk, order_key(l[j]));
         }
         mk = wave_max_u32(mk);
@@ -258,10 +259,17 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void route_backward_kernel(
         const int e = j * kWave + lane;
         if (e >= E) continue;
         if constexpr (kBf16)
-            ((uint16_t*)grad_logits)[(int64_t)t * E + e] = __builtin_bit_cast(uint16_t, (__bf16)out[j]);
+            ((uint16_t*)grad_logits)[t * E + e] = __builtin_bit_cast(uint16_t, (__bf16)out[j]);
         else
-            ((float*)grad_logits)[(int64_t)t * E + e] = out[j];
+            ((float*)grad_logits)[t * E + e] = out[j];
     }
+    }
+}
+
+unsigned route_blocks(int T)
+{
+    const int64_t blocks = ((int64_t)T + kRouteWaves - 1) / kRouteWaves;
+    return (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20);
 }
 
 template <int kPer>
@@ -269,7 +277,7 @@ void route_per(const void* logits, bool bf16, int T, int E, int K, bool sigmoid_
                const float* bias, int renorm, float scale, int32_t* topk_idx, float* topk_w,
                hipStream_t stream)
 {
-    const dim3 grid((unsigned)((T + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * kWave);
+    const dim3 grid(route_blocks(T)), block(kRouteWaves * kWave);
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, block, 0, stream, logits, bias, T, E, K, renorm, scale,
                            topk_idx, topk_w);
@@ -284,7 +292,7 @@ void route_backward_per(const void* logits, bool bf16, int T, int E, int K, bool
                         int renorm, float scale, const int32_t* topk_idx, const float* grad_w,
                         void* grad_logits, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((T + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * kWave);
+    const dim3 grid(route_blocks(T)), block(kRouteWaves * kWave);
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, block, 0, stream, logits, T, E, K, scale, topk_idx, grad_w,
                            grad_logits);

@@ -574,10 +574,11 @@ int ep_dispatch_backward(const uint16_t* grad_recv, const int32_t* row_of_pair, 
 /*
  * The experts' products with 4-bit weights, on receive rows in place: for the
  * rows r of expert e (expert_offset[e] <= r < expert_offset[e+1])
- *   acc[r, n] = sum over the 128-column blocks b, in ascending order, of
+ *   acc[r, n] = sum over the 128-column blocks b of
  *               (sum over c in b of x[r, c] * v(w[e][n, c]))
  *               * (w_scales[e][n, b] * x_scales[r, b])
- * in fp32, v the value of a code, and
+ * in fp32, v the value of a code (the order of the sums depends on the sizes
+ * only), and
  *   EP_ACT_NONE      out[r, n] = bf16_rne(acc[r, n]),  w has `outs` rows;
  *   EP_ACT_SILU_MUL  out[r, n] = bf16_rne(g / (1 + exp(-g)) * u) with
  *                    g = acc[r, n], u = acc[r, outs + n],  w has 2 * outs rows
@@ -597,7 +598,8 @@ int ep_dispatch_backward(const uint16_t* grad_recv, const int32_t* row_of_pair, 
  * Errors: EP_ENOTSUP for another payload; EP_EINVAL for another act, rows < 0,
  * E outside 1..1024, cols or outs not positive or not divisible as above,
  * NULL or misaligned pointers (x, w, out 16 B, the rest 4 B) when rows > 0,
- * or rows / 16 + min(rows, E) >= 65536 (a grid limit).
+ * cols > 2^24, or outs > 2^29 or so many rows and outputs that the launch
+ * would exceed 2^32 threads (from about rows * outs = 2^38 on).
  */
 #define EP_ACT_NONE 0
 #define EP_ACT_SILU_MUL 1
