@@ -35,37 +35,48 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kTile = 16;
 constexpr int kExpertWaves = 4;
-constexpr int kMaxExpertCols = 1 << 24;      // 64 rows of bf16 within 32-bit offsets
+constexpr int kMaxExpertCols = 1 << 23;      // 64 rows of bf16 within 31-bit offsets
+constexpr int64_t kMaxBuffer = 0x7FFFFFFF;
 
 // Row tile `idx` of the batch: its expert, first row and row count, from the
 // expert offsets (clamped to the rows there are).  False past the last tile.
-// Called by whole waves; the result is wave-uniform.  64 experts a round, one
-// per lane: tiles before each by a DPP scan, the expert that holds `idx` by a
-// ballot.
+// Called by whole waves; the result is wave-uniform.  Lane i counts the tiles
+// of E / 64 neighbouring experts (all offsets loaded before the first is used:
+// one round trip); a DPP scan gives the tiles before it.
 template <int kRows>
 __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ off, int E, int rows, int idx,
                                           int lane, int& expert, int& row0, int& count)
 {
-    int left = idx;
-    for (int e0 = 0; e0 < E; e0 += kWave) {
-        const int e = min(e0 + lane, E - 1);
-        int a = off[e], b = off[e + 1];
-        a = min(max(a, 0), rows);
-        b = min(max(b, a), rows);
-        const int tiles = e0 + lane < E ? (b - a + kRows - 1) / kRows : 0;
-        const int incl = wave_inclusive_scan(tiles);
-        const uint64_t past = __ballot(incl > left);
-        if (past) {
-            const int win = __builtin_ctzll(past);
-            left -= read_lane(incl - tiles, win);
-            expert = e0 + win;
-            row0 = read_lane(a, win) + left * kRows;
-            count = min(kRows, read_lane(b, win) - row0);
-            return true;
-        }
-        left -= read_lane(incl, kWave - 1);
+    constexpr int kMaxPer = kMaxExperts / kWave;
+    const int per = (E + kWave - 1) / kWave;
+    const int e0 = lane * per;
+    int o[kMaxPer + 1];
+#pragma unroll
+    for (int j = 0; j <= kMaxPer; ++j)
+        if (j <= per) o[j] = off[min(e0 + j, E)];
+    int tiles = 0;
+#pragma unroll
+    for (int j = 0; j <= kMaxPer; ++j) {
+        if (j > per) break;
+        o[j] = min(max(o[j], j > 0 ? o[j - 1] : 0), rows);
+        if (j > 0) tiles += (o[j] - o[j - 1] + kRows - 1) / kRows;
     }
-    return false;
+    const int incl = wave_inclusive_scan(tiles);
+    const uint64_t past = __ballot(incl > idx);
+    if (!past) return false;
+    const int win = __builtin_ctzll(past);
+    int left = idx - (incl - tiles), at = 0, first = 0, end = 0;      // lane `win`'s are the answer
+#pragma unroll
+    for (int j = 0; j < kMaxPer; ++j) {
+        if (j >= per) break;
+        const int n = (o[j + 1] - o[j] + kRows - 1) / kRows;
+        if (left >= 0 && left < n) { at = j; first = o[j] + left * kRows; end = o[j + 1]; }
+        left -= n;
+    }
+    expert = win * per + read_lane(at, win);
+    row0 = read_lane(first, win);
+    count = min(kRows, read_lane(end, win) - row0);
+    return true;
 }
 
 template <int kSel>
@@ -104,145 +115,185 @@ __device__ __forceinline__ v4f block_product(v4i w, const v4i (&x)[4])
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
+// Bounded loads: a uniform base and size, a 32-bit offset per lane and a
+// uniform one; what lies past the size reads as 0.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, int64_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0,
+                                             (int)(bytes < kMaxBuffer ? bytes : kMaxBuffer), 0x00020000);
+}
+
+__device__ __forceinline__ v4i load_b128(__amdgpu_buffer_rsrc_t r, int lane_offset, int offset)
+{
+    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, lane_offset, offset, 0));
+}
+
 // Few rows per expert: the weights are read once and bound the time, so the
 // work is split for loads in flight.  A workgroup of 8 waves takes 16 rows of
-// one expert and a share of the weight rows, 64 (silu: 32 + 32) at a time; its
-// waves split the columns, wave i taking blocks i, i + 8, ..., and always have
-// the next block's codes and rows in flight, across the groups of 64 too.  The
-// waves' sums are joined through LDS in wave order.  The scales of a group are
-// one contiguous piece of memory; they are copied to LDS transposed, a window
-// of at most 64 blocks at a time.
-constexpr int kStreamWaves = 8;
+// one expert and a share of the weight rows, 64 (silu: 32 + 32) at a time: a
+// group.  kSplit waves share a group, each with its own run of blocks; their
+// sums are joined through LDS in wave order (kSplit 1: nothing to join, and no
+// barrier).  A wave always has the codes and rows of its next block in flight,
+// across groups too.  The scales of its next 16 blocks are copied to a wave's
+// own part of LDS, transposed.
+constexpr int kStreamWaves = 4;
+constexpr int kStreamManyGroups = 4096, kStreamLongCols = 4096;
 constexpr int kGroupRows = 64;                    // weight rows per group: 4 operand tiles
 constexpr int kGroupTiles = kGroupRows / kTile;
-constexpr int kWindow = 64;                       // blocks whose scales are in LDS
-constexpr int kScaleRows = kGroupRows + kTile;    // weight rows, then fp8 rows
-constexpr int kScalePitch = kScaleRows + 4;
+constexpr int kWindow = 16;                       // blocks whose scales are in LDS
+constexpr int kScalePitch = kGroupRows + kTile + 4;   // weight rows, then fp8 rows
 
-template <bool kFp8, bool kSilu>
-__global__ __launch_bounds__(kStreamWaves * kWave, 4) void expert_stream_kernel(
+template <bool kFp8, bool kSilu, int kSplit>
+__global__ __launch_bounds__(kStreamWaves * kWave, kFp8 ? 4 : 3) void expert_stream_kernel(
     const uint8_t* __restrict__ x, const float* __restrict__ xs, int rows, int cols,
     const int32_t* __restrict__ off, int E, const uint8_t* __restrict__ w,
-    const float* __restrict__ ws, int outs, uint16_t* __restrict__ out, int n_groups, int n_split)
+    const float* __restrict__ ws, int outs, uint16_t* __restrict__ out, int n_groups,
+    int n_parts)
 {
-    __shared__ __attribute__((aligned(16))) float s_scale[2][kWindow * kScalePitch];
-    __shared__ v4f s_part[kStreamWaves][kGroupTiles][kWave];
-    const int lane = threadIdx.x % kWave, m = lane % kTile, q = lane / kTile;
-    const int wave = wave_uniform(threadIdx.x / kWave);
+    constexpr int kTeams = kStreamWaves / kSplit;                   // groups at a time
     constexpr int kOuts = kSilu ? kGroupRows / 2 : kGroupRows;      // outputs per group
+    constexpr int kHalf = kOuts / kTile;                            // operand tiles of results
+    __shared__ __attribute__((aligned(16))) float s_scale[kStreamWaves][kWindow * kScalePitch];
+    __shared__ v4f s_part[kSplit > 1 ? kStreamWaves : 1][kGroupTiles][kWave];
+    const int lane = threadIdx.x % kWave, m = lane % kTile, q = lane / kTile;
+    const int wave = wave_uniform(threadIdx.x / kWave), team = wave / kSplit, part = wave % kSplit;
     int expert, row0, count;
-    if (!find_tile<kTile>(off, E, rows, blockIdx.x / n_split, lane, expert, row0, count)) return;
-    const int g0 = blockIdx.x % n_split;
+    if (!find_tile<kTile>(off, E, rows, blockIdx.x / n_parts, lane, expert, row0, count)) return;
     const int blocks = cols / kScaleBlock;
-    const int windows = (blocks + kWindow - 1) / kWindow;
+    const int run = ((blocks + 1) / 2 + kSplit - 1) / kSplit * 2;   // blocks per wave, in pairs
+    const int b0 = min(part * run, blocks), b1 = min(b0 + run, blocks);
     const int64_t wrow0 = expert * (kSilu ? 2 * (int64_t)outs : (int64_t)outs);
-    // lanes past the last row or output read a valid one; what they compute is not stored
-    const uint8_t* const xb = x + (int64_t)row0 * cols * (kFp8 ? 1 : 2);
-    const uint32_t xo = (uint32_t)min(m, count - 1) * cols * (kFp8 ? 1 : 2) + q * (kFp8 ? 16 : 64);
+    const int64_t wrow_end = wrow0 + (kSilu ? 2 * (int64_t)outs : (int64_t)outs);
+    constexpr int kParts = kSilu ? 2 : 1;                           // gate and up rows
+    const int half_cols = cols / 2;
+    // lanes past the last row read a valid one; what they compute is not stored
+    constexpr int kRowBytes = kFp8 ? 1 : 2;
+    const __amdgpu_buffer_rsrc_t xr = buffer(x + (int64_t)row0 * cols * kRowBytes, (int64_t)count * cols * kRowBytes);
+    const __amdgpu_buffer_rsrc_t xsr = buffer(kFp8 ? xs + (int64_t)row0 * blocks : nullptr, kFp8 ? (int64_t)count * blocks * 4 : 0);
+    const int xo = min(m, count - 1) * cols * kRowBytes + q * (kFp8 ? 16 : 64);
+    const int wo = m * half_cols + q * 16;
 
-    constexpr int kXRegs = kFp8 ? 2 : 4;
-    struct Step { v4i w[kGroupTiles]; v4i x[kXRegs]; };
-    // weight row j * 16 + m of group g (silu: tiles 0, 1 gate, 2, 3 up)
-    auto weight_row = [&](int g, int r) {
-        const int h = kSilu ? r / kOuts : 0;
-        return wrow0 + (int64_t)h * outs + min(g * kOuts + (kSilu ? r % kOuts : r), outs - 1);
-    };
-    auto load = [&](Step& s, int g, int b) {
+    // first weight row of part h of group g
+    auto weight_row = [&](int g, int h) { return wrow0 + (int64_t)h * outs + (int64_t)g * kOuts; };
+    // the codes of two neighbouring blocks: 128 bytes of every row
+    struct Codes { v4i w[2][kGroupTiles]; };
+    auto load = [&](Codes& s, int g, int b) {
 #pragma unroll
-        for (int j = 0; j < kGroupTiles; ++j)
-            s.w[j] = *(const v4i*)(w + weight_row(g, j * kTile + m) * (cols / 2) + b * 64 + q * 16);
+        for (int h = 0; h < kParts; ++h) {
+            const int64_t r = weight_row(g, h);
+            const __amdgpu_buffer_rsrc_t wr = buffer(w + r * half_cols, (wrow_end - r) * half_cols);
 #pragma unroll
-        for (int i = 0; i < kXRegs; ++i)
-            s.x[i] = *(const v4i*)(xb + xo + b * (kFp8 ? 128 : 256) + i * (kFp8 ? 64 : 16));
-    };
-    // the scales of 10 rows per wave, lane = block of the window
-    constexpr int kMine = kFp8 ? kScaleRows / kStreamWaves : kGroupRows / kStreamWaves;
-    float sc[kMine];
-    auto load_scales = [&](int g, int win) {
-        const int b = win * kWindow + lane;
+            for (int j = 0; j < kHalf; ++j)
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int r = i * kStreamWaves + wave;
-            const float* p = r < kGroupRows ? ws + weight_row(g, r) * blocks
-                                            : xs + (int64_t)(row0 + min(r - kGroupRows, count - 1)) * blocks;
-            sc[i] = b < blocks ? p[b] : 0.0f;
+                for (int i = 0; i < 2; ++i)
+                    s.w[i][h * kHalf + j] = load_b128(wr, wo, j * kTile * half_cols + min(b + i, blocks - 1) * 64);
         }
     };
-    auto store_scales = [&](int buf) {
+    constexpr int kXRegs = kFp8 ? 2 : 4;
+    auto load_x = [&](v4i (&v)[kXRegs], int b) {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) s_scale[buf][lane * kScalePitch + i * kStreamWaves + wave] = sc[i];
+        for (int i = 0; i < kXRegs; ++i)
+            v[i] = load_b128(xr, xo, b * (kFp8 ? 128 : 256) + i * (kFp8 ? 64 : 16));
+    };
+    float* const sc = s_scale[wave];
+    // Scales of blocks b .. b + 15: 16 rows per load, 4 blocks per lane.  No use
+    // is made of a load that is partly past its buffer: a lane's 4 blocks end
+    // at the row's last one at most (rows of fewer than 4 blocks: one per lane).
+    auto stage_scales = [&](int g, int b) {
+        const bool wide = blocks >= 4;
+        const int bl = wide ? min(b + (lane % 4) * 4, blocks - 4) : min(b + lane % 4, blocks - 1);
+        const int so = ((lane / 4) * blocks + bl) * 4;
+        v4f v[kGroupTiles + 1];
+        auto get = [&](__amdgpu_buffer_rsrc_t r, int offset) {
+            if (wide) return __builtin_bit_cast(v4f, load_b128(r, so, offset));
+            const v4i one = {(int)__builtin_amdgcn_raw_buffer_load_b32(r, so, offset, 0), 0, 0, 0};
+            return __builtin_bit_cast(v4f, one);
+        };
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+            const int64_t r = weight_row(g, h);
+            const __amdgpu_buffer_rsrc_t sr = buffer(ws + r * blocks, (wrow_end - r) * blocks * 4);
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) v[h * kHalf + j] = get(sr, j * kTile * blocks * 4);
+        }
+        if constexpr (kFp8) v[kGroupTiles] = get(xsr, 0);
+        wave_lds_sync();
+        const int at = bl - b;                             // negative: blocks before the window
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (at + i < 0 || (i > 0 && !wide)) continue;
+#pragma unroll
+            for (int j = 0; j < kGroupTiles + (kFp8 ? 1 : 0); ++j)
+                sc[(at + i) * kScalePitch + j * kTile + lane / 4] = v[j][i];
+        }
+        wave_lds_sync();
     };
 
-    if (g0 >= n_groups) return;
-    Step cur, next;
-    load_scales(g0, 0);
-    if (wave < blocks) load(cur, g0, wave);
-    store_scales(0);
-    __syncthreads();
-    int buf = 0;
-    for (int g = g0; g < n_groups; g += n_split) {
-        v4f acc[kGroupTiles];
+    const int g = (blockIdx.x % n_parts) * kTeams + team;
+    v4f acc[kGroupTiles];
 #pragma unroll
-        for (int j = 0; j < kGroupTiles; ++j) acc[j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-        for (int win = 0; win < windows; ++win) {
-            const bool last = win + 1 == windows;
-            const int g_next = last ? g + n_split : g;
-            const bool more = g_next < n_groups;
-            if (more) load_scales(g_next, last ? 0 : win + 1);
-            const int end = min(blocks, (win + 1) * kWindow);
-            for (int b = win * kWindow + wave; b < end; b += kStreamWaves) {
-                // the block after this one, in this window, the next or the next group
-                const int bn = b + kStreamWaves;
-                if (bn < blocks) load(next, g, bn);
-                else if (g + n_split < n_groups) load(next, g + n_split, wave);
-                const float* const sb = s_scale[buf] + (b - win * kWindow) * kScalePitch;
+    for (int j = 0; j < kGroupTiles; ++j) acc[j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    if (g < n_groups && b0 < b1) {
+        Codes cur, next;
+        load(cur, g, b0);
+        for (int b = b0; b < b1; b += 2) {
+            const int at = (b - b0) % kWindow;
+            if (at == 0) stage_scales(g, b);
+            v4i xv[2][kXRegs];
+            load_x(xv[0], b);
+            load_x(xv[1], min(b + 1, blocks - 1));
+            if (b + 2 < b1) load(next, g, b + 2);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (b + u >= b1) break;
+                const float* const sb = sc + (at + u) * kScalePitch;
                 const float f = kFp8 ? sb[kGroupRows + m] : 1.0f;
 #pragma unroll
                 for (int j = 0; j < kGroupTiles; ++j) {
                     const v4f sw = *(const v4f*)(sb + j * kTile + q * 4);
                     v4f d;
                     if constexpr (kFp8) {
-                        const v8i xv = {cur.x[0][0], cur.x[0][1], cur.x[0][2], cur.x[0][3],
-                                        cur.x[1][0], cur.x[1][1], cur.x[1][2], cur.x[1][3]};
-                        d = block_product(cur.w[j], xv);
+                        const v8i x8 = {xv[u][0][0], xv[u][0][1], xv[u][0][2], xv[u][0][3],
+                                        xv[u][1][0], xv[u][1][1], xv[u][1][2], xv[u][1][3]};
+                        d = block_product(cur.w[u][j], x8);
                     } else {
-                        d = block_product(cur.w[j], cur.x);
+                        d = block_product(cur.w[u][j], xv[u]);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] = __builtin_fmaf(d[i], sw[i] * f, acc[j][i]);
                 }
-                cur = next;
             }
-            buf ^= 1;
-            if (more) store_scales(buf);
-            if (last)
-#pragma unroll
-                for (int j = 0; j < kGroupTiles; ++j) s_part[wave][j][lane] = acc[j];
-            lds_barrier();
+            cur = next;
         }
-        // two neighbouring outputs per thread: lane's quarter `half` of operand tile j
-        const int idx = threadIdx.x / 2, half = threadIdx.x % 2;
-        const int j = idx / kWave, ln = idx % kWave;
-        if (j < kOuts / kTile) {
-            float v[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
+    }
+    // operand tile j of lane ln: row ln % 16, outputs (ln / 16) * 4 .. + 3 of the tile
+    auto store = [&](int j, int ln, v4f v, v4f u) {
+        const int r = ln % kTile, n = g * kOuts + j * kTile + (ln / kTile) * 4;
+        if (r >= count || n >= outs) return;
+        if constexpr (kSilu)
 #pragma unroll
-            for (int i = 0; i < kStreamWaves; ++i) {
-                const float* const p = (const float*)&s_part[i][j][ln] + half * 2;
-                v[0] += p[0];
-                v[1] += p[1];
-                if constexpr (kSilu) {
-                    const float* const pu = (const float*)&s_part[i][j + kOuts / kTile][ln] + half * 2;
-                    u[0] += pu[0];
-                    u[1] += pu[1];
-                }
-            }
-            const int r = ln % kTile, n = g * kOuts + j * kTile + (ln / kTile) * 4 + half * 2;
-            if (r < count && n < outs) {
-                if constexpr (kSilu) { v[0] = silu_mul(v[0], u[0]); v[1] = silu_mul(v[1], u[1]); }
-                *(uint32_t*)(out + (int64_t)(row0 + r) * outs + n) = pack2_bf16(v[0], v[1]);
-            }
-        }
+            for (int i = 0; i < 4; ++i) v[i] = silu_mul(v[i], u[i]);
+        store8<false>(out + (int64_t)(row0 + r) * outs + n,
+                      make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])));
+    };
+    if constexpr (kSplit == 1) {
+        if (g < n_groups)
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) store(j, lane, acc[j], kSilu ? acc[j + kHalf] : acc[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kGroupTiles; ++j) s_part[wave][j][lane] = acc[j];
         lds_barrier();
+        // the team's waves take its result tiles in turn
+        for (int j = part; j < kHalf; j += kSplit) {
+            v4f v = {0.0f, 0.0f, 0.0f, 0.0f}, u = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+            for (int i = 0; i < kSplit; ++i) {
+                v += s_part[team * kSplit + i][j][lane];
+                if constexpr (kSilu) u += s_part[team * kSplit + i][j + kHalf][lane];
+            }
+            if (g < n_groups) store(j, lane, v, u);
+        }
     }
 }
 
@@ -254,8 +305,10 @@ __global__ __launch_bounds__(kStreamWaves * kWave, 4) void expert_stream_kernel(
 constexpr int kWaveCols = 64;                    // weight rows per wave: 4 operand tiles
 constexpr int kColTiles = kWaveCols / kTile;
 
+constexpr int kTileRows = 64;                    // rows per workgroup
+
 template <bool kFp8> struct TileShape {
-    static constexpr int kRows = 64;                         // rows per workgroup
+    static constexpr int kRows = kTileRows;
     static constexpr int kRowTiles = kRows / kTile;
     static constexpr int kBlockBytes = kScaleBlock * (kFp8 ? 1 : 2);
     static constexpr int kPieces = kRows * kBlockBytes / 1024 / kExpertWaves;   // 1 KB loads per wave
@@ -429,27 +482,45 @@ int64_t max_tiles(int rows, int E, int height)
     return (int64_t)rows / height + (rows < E ? rows : E);
 }
 
-constexpr int64_t kStreamBlocks = 4096;
-
 // Few rows per expert: the kernel that streams the weights; more: the tiles.
 bool expert_large(int rows, int E) { return rows > 8 * (int64_t)E; }
 
-int64_t tile_blocks(bool fp8, bool silu, int rows, int outs, int E)
+int64_t tile_blocks(bool silu, int rows, int outs, int E)
 {
     const int per = kExpertWaves * (silu ? kWaveCols / 2 : kWaveCols);
     const int64_t groups = ((int64_t)outs + per - 1) / per;
-    const int64_t tiles = max_tiles(rows, E, fp8 ? TileShape<true>::kRows : TileShape<false>::kRows);
-    return (tiles + kXcds - 1) / kXcds * kXcds * groups;
+    return (max_tiles(rows, E, kTileRows) + kXcds - 1) / kXcds * kXcds * groups;
+}
+
+int stream_groups(bool silu, int outs)
+{
+    const int per = silu ? kGroupRows / 2 : kGroupRows;
+    return (int)(((int64_t)outs + per - 1) / per);
+}
+
+// Waves that share a group in the streaming kernel.
+int stream_split(bool silu, int rows, int cols, int outs, int E)
+{
+    const bool many = max_tiles(rows, E, kTile) * stream_groups(silu, outs) >= kStreamManyGroups;
+    return many && cols < kStreamLongCols ? 1 : kStreamWaves;
+}
+
+int64_t stream_blocks(bool silu, int rows, int cols, int outs, int E)
+{
+    const int teams = kStreamWaves / stream_split(silu, rows, cols, outs, E);
+    return max_tiles(rows, E, kTile) * ((stream_groups(silu, outs) + teams - 1) / teams);
 }
 
 }  // namespace
 
-bool expert_launch_ok(bool fp8, bool silu, int rows, int cols, int outs, int E)
+bool expert_launch_ok(bool silu, int rows, int cols, int outs, int E)
 {
     // offsets within a tile are 32-bit; a grid dimension holds fewer than 2^32 threads
     if (cols > kMaxExpertCols || outs > (1 << 29)) return false;
-    if (!expert_large(rows, E)) return true;       // at most kStreamBlocks + max_tiles workgroups
-    return tile_blocks(fp8, silu, rows, outs, E) * kExpertWaves * kWave < ((int64_t)1 << 32);
+    static_assert(kExpertWaves == kStreamWaves, "both kernels launch the same workgroups");
+    const int64_t blocks = expert_large(rows, E) ? tile_blocks(silu, rows, outs, E)
+                                                 : stream_blocks(silu, rows, cols, outs, E);
+    return blocks * kExpertWaves * kWave < ((int64_t)1 << 32);
 }
 
 hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int rows, int cols,
@@ -461,7 +532,7 @@ hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int row
     if (expert_large(rows, E)) {
         const int per = kExpertWaves * (silu ? kWaveCols / 2 : kWaveCols);
         const int groups = (outs + per - 1) / per;
-        const dim3 grid((unsigned)tile_blocks(fp8, silu, rows, outs, E));
+        const dim3 grid((unsigned)tile_blocks(silu, rows, outs, E));
         auto go = [&](auto kernel) {
             hipLaunchKernelGGL(kernel, grid, block, 0, stream, (const uint8_t*)x, x_scales, rows,
                                cols, expert_offset, E, w, w_scales, outs, out, groups);
@@ -470,19 +541,20 @@ hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int row
         else silu ? go(expert_tile_kernel<false, true>) : go(expert_tile_kernel<false, false>);
         return hipGetLastError();
     }
-    const int per = silu ? kGroupRows / 2 : kGroupRows;
-    const int groups = (outs + per - 1) / per;
-    const int64_t tiles = max_tiles(rows, E, kTile);
-    // about kStreamBlocks workgroups: several rounds of the 512 that run at once
-    const int split = (int)std::min<int64_t>(groups, (kStreamBlocks + tiles - 1) / tiles);
-    const dim3 grid((unsigned)(tiles * split));
+    const int split = stream_split(silu, rows, cols, outs, E);
+    const int groups = stream_groups(silu, outs), teams = kStreamWaves / split;
+    const dim3 grid((unsigned)stream_blocks(silu, rows, cols, outs, E));
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(kStreamWaves * kWave), 0, stream, (const uint8_t*)x,
-                           x_scales, rows, cols, expert_offset, E, w, w_scales, outs, out, groups,
-                           split);
+        hipLaunchKernelGGL(kernel, grid, block, 0, stream, (const uint8_t*)x, x_scales, rows, cols,
+                           expert_offset, E, w, w_scales, outs, out, groups, (groups + teams - 1) / teams);
     };
-    if (fp8) silu ? go(expert_stream_kernel<true, true>) : go(expert_stream_kernel<true, false>);
-    else silu ? go(expert_stream_kernel<false, true>) : go(expert_stream_kernel<false, false>);
+    auto pick = [&](auto sp) {
+        constexpr int kS = decltype(sp)::value;
+        if (fp8) silu ? go(expert_stream_kernel<true, true, kS>) : go(expert_stream_kernel<true, false, kS>);
+        else silu ? go(expert_stream_kernel<false, true, kS>) : go(expert_stream_kernel<false, false, kS>);
+    };
+    if (split == 1) pick(std::integral_constant<int, 1>());
+    else pick(std::integral_constant<int, kStreamWaves>());
     return hipGetLastError();
 }
 
