@@ -297,22 +297,61 @@ __global__ __launch_bounds__(kStreamWaves * kWave, kFp8 ? 4 : 3) void expert_str
     }
 }
 
-// Large batches: a workgroup computes up to kTileRows rows x 4 * kWaveCols
-// weight rows.  Every wave has its own weight rows, loaded straight into
-// registers (no other wave needs them), and all the rows: those go through
-// LDS, one 128-column block at a time, double buffered, loaded one block
-// ahead.  Row groups of 16 past the last row are skipped.
+// Large batches: a workgroup computes up to 64 rows x 256 weight rows, 64 of
+// them per wave.  Codes, rows and scales go from memory straight to LDS, a
+// ring of stages of one block each, kStages - 1 of them in flight; every wave
+// loads its own codes and a quarter of the rows, waits for its own loads of
+// the oldest stage and meets the others at one barrier per block.
+//
+// A load of 16 bytes per lane covers whole rows of the block (codes: 16 rows x
+// 64 bytes; fp8 rows: 8 x 128; bf16: 4 x 256), and the 16-byte pieces of a row
+// are permuted (piece ^ row bits) so that 8 lanes reading one piece of 8
+// neighbouring rows meet 8 different banks.
 constexpr int kWaveCols = 64;                    // weight rows per wave: 4 operand tiles
 constexpr int kColTiles = kWaveCols / kTile;
-
 constexpr int kTileRows = 64;                    // rows per workgroup
+constexpr int kRowTiles = kTileRows / kTile;
 
-template <bool kFp8> struct TileShape {
-    static constexpr int kRows = kTileRows;
-    static constexpr int kRowTiles = kRows / kTile;
-    static constexpr int kBlockBytes = kScaleBlock * (kFp8 ? 1 : 2);
-    static constexpr int kPieces = kRows * kBlockBytes / 1024 / kExpertWaves;   // 1 KB loads per wave
+template <bool kFp8> struct TileStage {
+    static constexpr int kRowBytes = kScaleBlock * (kFp8 ? 1 : 2);
+    static constexpr int kRowsPerLoad = 1024 / kRowBytes;
+    static constexpr int kXLoads = kTileRows / kRowsPerLoad / kExpertWaves;      // per wave
+    static constexpr int kLoads = kXLoads + kColTiles + 1 + (kFp8 ? 1 : 0);     // per wave and stage
+    static constexpr int kStages = kFp8 ? 3 : 2;
+    uint8_t w[kExpertWaves][kWaveCols * kScaleBlock / 2];
+    uint8_t x[kTileRows * kRowBytes];
+    float ws[kExpertWaves][kWaveCols];
+    float xs[kExpertWaves][kFp8 ? kTileRows : 4];
 };
+
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, void* lds, int lane_offset, int offset)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
+                                             lane_offset, offset, 0, 0);
+}
+
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, void* lds, int lane_offset, int offset)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4,
+                                             lane_offset, offset, 0, 0);
+}
+
+// Waits until at most kOutstanding of this wave's loads are in flight (they
+// complete in order) and its LDS reads are done, and meets the workgroup: then
+// the older loads of every wave are in LDS and what was read before may be
+// overwritten.  A workgroup fence in place of the empty asm statements, which
+// only keep the compiler from moving accesses across, would wait for every
+// load in flight into LDS.
+template <int kOutstanding>
+__device__ __forceinline__ void stage_barrier()
+{
+    static_assert(kOutstanding >= 0 && kOutstanding < 64, "vmcnt holds 6 bits");
+    asm volatile("" ::: "memory");
+    // gfx9 encoding: vmcnt in bits 3:0 and 15:14, expcnt in 6:4 (not waited for), lgkmcnt 0 in 11:8
+    __builtin_amdgcn_s_waitcnt((kOutstanding & 15) | ((kOutstanding >> 4) << 14) | 0x70);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 
 template <bool kFp8, bool kSilu>
 __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
@@ -320,104 +359,86 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
     const int32_t* __restrict__ off, int E, const uint8_t* __restrict__ w,
     const float* __restrict__ ws, int outs, uint16_t* __restrict__ out, int n_groups)
 {
-    using S = TileShape<kFp8>;
-    __shared__ __attribute__((aligned(16))) uint8_t s_x[2][S::kRows * S::kBlockBytes];
-    __shared__ float s_xs[2][kFp8 ? S::kRows : 1];
-    __shared__ __attribute__((aligned(16))) float s_ws[2][kExpertWaves][kWaveCols];
+    using S = TileStage<kFp8>;
+    __shared__ __attribute__((aligned(16))) S ring[S::kStages];
     const int lane = threadIdx.x % kWave, m = lane % kTile, q = lane / kTile;
     const int wave = wave_uniform(threadIdx.x / kWave);
     // the column groups of one row tile on one XCD (they share its rows)
     const int slot = blockIdx.x / kXcds;
     const int tile = (slot / n_groups) * kXcds + blockIdx.x % kXcds;
-    constexpr int kOuts = kSilu ? kWaveCols / 2 : kWaveCols;   // outputs per wave
+    constexpr int kParts = kSilu ? 2 : 1;                      // gate and up rows
+    constexpr int kOuts = kWaveCols / kParts;                  // outputs per wave
+    constexpr int kHalf = kOuts / kTile;                       // operand tiles of a part
     const int n0 = ((slot % n_groups) * kExpertWaves + wave) * kOuts;
     int expert, row0, count;
-    if (!find_tile<S::kRows>(off, E, rows, tile, lane, expert, row0, count)) return;
+    if (!find_tile<kTileRows>(off, E, rows, tile, lane, expert, row0, count)) return;
     const int live = (count + kTile - 1) / kTile;
-    const int blocks = cols / kScaleBlock;
-    const int64_t wrows = kSilu ? 2 * (int64_t)outs : outs;
+    const int blocks = cols / kScaleBlock, half_cols = cols / 2;
+    const int64_t wrows = (int64_t)outs * kParts;
 
-    // operand tile j: weight rows n0 + 16 j (silu: two of the gate, then the two of the up rows)
-    // (a uniform base and a 32-bit offset per lane, which stays below 16 rows)
-    const uint8_t* wp[kColTiles];
-    int wo[kColTiles];
+    // codes: load j is operand tile j, lane i piece i % 4 of row i / 4 (past the
+    // last output: other rows or 0, not stored)
+    __amdgpu_buffer_rsrc_t wr[kParts], sr[kParts];
 #pragma unroll
-    for (int j = 0; j < kColTiles; ++j) {
-        const int h = kSilu ? j / 2 : 0, t = kSilu ? j % 2 : j;
-        const int n = min(n0 + t * kTile, outs - 1);
-        wp[j] = w + (expert * wrows + (int64_t)h * outs + n) * (cols / 2);
-        wo[j] = min(m, outs - 1 - n) * (cols / 2) + q * 16;
+    for (int h = 0; h < kParts; ++h) {
+        const int64_t r = min((int64_t)n0, (int64_t)outs) + (int64_t)h * outs;
+        wr[h] = buffer(w + (expert * wrows + r) * half_cols, (wrows - r) * half_cols);
+        sr[h] = buffer(ws + (expert * wrows + r) * blocks, (wrows - r) * blocks * 4);
     }
-    // lane i of a wave stages the scale of weight row (i / 16, i % 16) of its tiles
-    const float* wsp;
-    {
-        const int h = kSilu ? q / 2 : 0, t = kSilu ? q % 2 : q;
-        wsp = ws + (expert * wrows + (int64_t)h * outs + min(n0 + t * kTile + m, outs - 1)) * blocks;
-    }
-    // a wave stages row tile `wave`; fp8: piece p is half p of its operand, in
-    // operand order; bf16: rows 4 p .. 4 p + 3, 16-byte pieces of row r at r ^ piece
-    const uint8_t* const xp = x + (int64_t)row0 * cols * (kFp8 ? 1 : 2);
-    int xo[S::kPieces];
-    int xdst[S::kPieces];
-    const bool xlive = wave < live;
+    const int wo = (lane / 4) * half_cols + ((lane % 4) ^ ((lane / 8) % 4)) * 16;
+    // scales: lane i that of weight row i of the wave; silu: lanes 32 .. 63 the up rows
+    const int so = (kSilu ? lane % kOuts : lane) * blocks * 4;
+    // rows past the last are read as the last one; what they give is not stored
+    const __amdgpu_buffer_rsrc_t xr = buffer(x + (int64_t)row0 * cols * (S::kRowBytes / kScaleBlock),
+                                             (int64_t)count * cols * (S::kRowBytes / kScaleBlock));
+    const __amdgpu_buffer_rsrc_t xsr = buffer(kFp8 ? xs + (int64_t)row0 * blocks : nullptr,
+                                              kFp8 ? (int64_t)count * blocks * 4 : 0);
+    int xo[S::kXLoads];
 #pragma unroll
-    for (int p = 0; p < S::kPieces; ++p) {
-        if constexpr (kFp8) {
-            xo[p] = min(wave * kTile + m, count - 1) * cols + p * 64 + q * 16;
-            xdst[p] = (wave * 2 + p) * 1024 + lane * 16;
-        } else {
-            const int r = wave * kTile + p * 4 + q;
-            xo[p] = min(r, count - 1) * cols * 2 + m * 16;
-            xdst[p] = r * 256 + ((m ^ (r % kTile)) * 16);
-        }
+    for (int p = 0; p < S::kXLoads; ++p) {
+        constexpr int kPieces = S::kRowBytes / 16;
+        const int r = (wave * S::kXLoads + p) * S::kRowsPerLoad + lane / kPieces;
+        const int piece = (lane % kPieces) ^ (r % kPieces);
+        xo[p] = min(r, count - 1) * cols * (S::kRowBytes / kScaleBlock) + piece * 16;
     }
-    const int xs_row = threadIdx.x;                 // fp8: thread i stages the scale of row i
-    const float* const xsp = kFp8 ? xs + (int64_t)(row0 + min(xs_row, count - 1)) * blocks : nullptr;
-
-    v4i xr[S::kPieces], wr[kColTiles];
-    float xsr = 0.0f, wsr;
-    auto load = [&](int b) {
+    const int xso = min(lane, count - 1) * blocks * 4;
+    auto load = [&](S& s, int b) {
+        b = min(b, blocks - 1);                  // past the end: loads that nobody reads
 #pragma unroll
-        for (int p = 0; p < S::kPieces; ++p)
-            if (xlive) xr[p] = *(const v4i*)(xp + (int64_t)b * S::kBlockBytes + (uint32_t)xo[p]);
-        if constexpr (kFp8) if (xs_row < S::kRows) xsr = xsp[b];
-        wsr = wsp[b];
+        for (int p = 0; p < S::kXLoads; ++p)
+            load_lds16(xr, s.x + (wave * S::kXLoads + p) * 1024, xo[p], b * S::kRowBytes);
+#pragma unroll
+        for (int h = 0; h < kParts; ++h)
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j)
+                load_lds16(wr[h], s.w[wave] + (h * kHalf + j) * 1024, wo, j * kTile * half_cols + b * 64);
+        if constexpr (!kSilu) load_lds4(sr[0], s.ws[wave], so, b * 4);
+        else load_lds4(sr[0], s.ws[wave], so + (lane / kOuts) * outs * blocks * 4, b * 4);
+        if constexpr (kFp8) load_lds4(xsr, s.xs[wave], xso, b * 4);
     };
-    auto load_w = [&](int b) {
+    v4f acc[kRowTiles][kColTiles];
 #pragma unroll
-        for (int j = 0; j < kColTiles; ++j) wr[j] = *(const v4i*)(wp[j] + (int64_t)b * 64 + (uint32_t)wo[j]);
-    };
-    v4f acc[S::kRowTiles][kColTiles];
-#pragma unroll
-    for (int t = 0; t < S::kRowTiles; ++t)
+    for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
         for (int j = 0; j < kColTiles; ++j) acc[t][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 
-    load(0);
-    load_w(0);
-    for (int b = 0; b < blocks; ++b) {
-        const int buf = b & 1;
-#pragma unroll
-        for (int p = 0; p < S::kPieces; ++p)
-            if (xlive) *(v4i*)(s_x[buf] + xdst[p]) = xr[p];
-        if constexpr (kFp8) if (xs_row < S::kRows) s_xs[buf][xs_row] = xsr;
-        s_ws[buf][wave][lane] = wsr;
-        lds_barrier();
+    auto compute = [&](const S& s) {
         v4i wc[kColTiles];
-#pragma unroll
-        for (int j = 0; j < kColTiles; ++j) wc[j] = wr[j];
-        if (b + 1 < blocks) { load(b + 1); load_w(b + 1); }
         v4f sw[kColTiles];
 #pragma unroll
-        for (int j = 0; j < kColTiles; ++j) sw[j] = *(const v4f*)&s_ws[buf][wave][j * kTile + q * 4];
+        for (int j = 0; j < kColTiles; ++j) {
+            wc[j] = *(const v4i*)(s.w[wave] + j * 1024 + m * 64 + (q ^ ((m / 2) % 4)) * 16);
+            sw[j] = *(const v4f*)&s.ws[wave][j * kTile + q * 4];
+        }
         if constexpr (kFp8) {
 #pragma unroll
-            for (int t = 0; t < S::kRowTiles; ++t) {
+            for (int t = 0; t < kRowTiles; ++t) {
                 if (t >= live) break;
-                const v4i lo = *(const v4i*)(s_x[buf] + t * 2048 + lane * 16);
-                const v4i hi = *(const v4i*)(s_x[buf] + t * 2048 + 1024 + lane * 16);
+                const uint8_t* const xrow = s.x + (t * kTile + m) * 128;
+                const v4i lo = *(const v4i*)(xrow + (q ^ (m % 8)) * 16);
+                const v4i hi = *(const v4i*)(xrow + ((4 + q) ^ (m % 8)) * 16);
                 const v8i xb = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                const float f = s_xs[buf][t * kTile + m];
+                const float f = s.xs[wave][t * kTile + m];
                 v4f d[kColTiles];
 #pragma unroll
                 for (int j = 0; j < kColTiles; ++j) d[j] = block_product(wc[j], xb);
@@ -432,40 +453,52 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
 #pragma unroll
             for (int j = 0; j < kColTiles; ++j)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) wb[j][s] = bf16x8_of_codes((uint32_t)wc[j][s]);
+                for (int i = 0; i < 4; ++i) wb[j][i] = bf16x8_of_codes((uint32_t)wc[j][i]);
 #pragma unroll
-            for (int t = 0; t < S::kRowTiles; ++t) {
+            for (int t = 0; t < kRowTiles; ++t) {
                 if (t >= live) break;
                 v8bf xb[4];
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    xb[s] = *(const v8bf*)(s_x[buf] + (t * kTile + m) * 256 + (((q * 4 + s) ^ m) * 16));
+                for (int i = 0; i < 4; ++i)
+                    xb[i] = *(const v8bf*)(s.x + (t * kTile + m) * 256 + ((q * 4 + i) ^ m) * 16);
 #pragma unroll
                 for (int j = 0; j < kColTiles; ++j) {
                     v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][s], xb[s], d, 0, 0, 0);
+                    for (int i = 0; i < 4; ++i)
+                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][i], xb[i], d, 0, 0, 0);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         acc[t][j][i] = __builtin_fmaf(d[i], sw[j][i], acc[t][j][i]);
                 }
             }
         }
-    }
+    };
+
+    constexpr int kAhead = S::kStages - 1;
 #pragma unroll
-    for (int t = 0; t < S::kRowTiles; ++t) {
+    for (int i = 0; i < kAhead; ++i) load(ring[i], i);
+    int at = 0;
+    for (int b = 0; b < blocks; ++b) {
+        stage_barrier<(kAhead - 1) * S::kLoads>();
+        load(ring[at == 0 ? kAhead : at - 1], b + kAhead);      // the stage read last
+        compute(ring[at]);
+        at = at + 1 == S::kStages ? 0 : at + 1;
+    }
+    stage_barrier<0>();                          // nothing in flight into LDS when the wave ends
+#pragma unroll
+    for (int t = 0; t < kRowTiles; ++t) {
         const int r = t * kTile + m;
         if (r >= count) continue;
         uint16_t* const orow = out + (int64_t)(row0 + r) * outs;
 #pragma unroll
-        for (int j = 0; j < (kSilu ? kColTiles / 2 : kColTiles); ++j) {
+        for (int j = 0; j < kHalf; ++j) {
             const int n = n0 + j * kTile + q * 4;
             if (n >= outs) continue;
             float v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[i] = kSilu ? silu_mul(acc[t][j][i], acc[t][j + kColTiles / 2][i]) : acc[t][j][i];
+                v[i] = kSilu ? silu_mul(acc[t][j][i], acc[t][(j + kHalf) % kColTiles][i]) : acc[t][j][i];
             store8<false>(orow + n, make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])));
         }
     }
@@ -518,6 +551,7 @@ bool expert_launch_ok(bool silu, int rows, int cols, int outs, int E)
     // offsets within a tile are 32-bit; a grid dimension holds fewer than 2^32 threads
     if (cols > kMaxExpertCols || outs > (1 << 29)) return false;
     static_assert(kExpertWaves == kStreamWaves, "both kernels launch the same workgroups");
+    if (silu && (int64_t)outs * cols >= ((int64_t)1 << 36)) return false;
     const int64_t blocks = expert_large(rows, E) ? tile_blocks(silu, rows, outs, E)
                                                  : stream_blocks(silu, rows, cols, outs, E);
     return blocks * kExpertWaves * kWave < ((int64_t)1 << 32);

@@ -598,8 +598,9 @@ int ep_dispatch_backward(const uint16_t* grad_recv, const int32_t* row_of_pair, 
  * Errors: EP_ENOTSUP for another payload; EP_EINVAL for another act, rows < 0,
  * E outside 1..1024, cols or outs not positive or not divisible as above,
  * NULL or misaligned pointers (x, w, out 16 B, the rest 4 B) when rows > 0,
- * cols > 2^24, or outs > 2^29 or so many rows and outputs that the launch
- * would exceed 2^32 threads (from about rows * outs = 2^38 on).
+ * or sizes past the kernels' offsets and grids: cols > 2^23, outs > 2^29,
+ * outs * cols >= 2^36 with EP_ACT_SILU_MUL, or a launch of 2^32 threads or
+ * more (from about rows * outs = 2^38 on).
  */
 #define EP_ACT_NONE 0
 #define EP_ACT_SILU_MUL 1
