@@ -298,10 +298,12 @@ __global__ __launch_bounds__(kStreamWaves * kWave, kFp8 ? 4 : 3) void expert_str
 }
 
 // Large batches: a workgroup computes up to 64 rows x 256 weight rows, 64 of
-// them per wave.  Codes, rows and scales go from memory straight to LDS, a
-// ring of stages of one block each, kStages - 1 of them in flight; every wave
-// loads its own codes and a quarter of the rows, waits for its own loads of
-// the oldest stage and meets the others at one barrier per block.
+// them per wave.  Codes and rows go from memory straight to LDS, a ring of
+// stages of one block each, kStages - 1 of them in flight; every wave loads its
+// own codes and a quarter of the rows, waits for its own loads of the oldest
+// stage and meets the others at one barrier per block.  Scales are loaded for
+// 4 blocks at a time (16 bytes of one row per lane: block by block they would
+// be one 4-byte piece of 64 lines) and kept in LDS transposed.
 //
 // A load of 16 bytes per lane covers whole rows of the block (codes: 16 rows x
 // 64 bytes; fp8 rows: 8 x 128; bf16: 4 x 256), and the 16-byte pieces of a row
@@ -316,23 +318,24 @@ template <bool kFp8> struct TileStage {
     static constexpr int kRowBytes = kScaleBlock * (kFp8 ? 1 : 2);
     static constexpr int kRowsPerLoad = 1024 / kRowBytes;
     static constexpr int kXLoads = kTileRows / kRowsPerLoad / kExpertWaves;      // per wave
-    static constexpr int kLoads = kXLoads + kColTiles + 1 + (kFp8 ? 1 : 0);     // per wave and stage
+    static constexpr int kLoads = kXLoads + kColTiles;                           // per wave and stage
     static constexpr int kStages = kFp8 ? 3 : 2;
     uint8_t w[kExpertWaves][kWaveCols * kScaleBlock / 2];
     uint8_t x[kTileRows * kRowBytes];
-    float ws[kExpertWaves][kWaveCols];
-    float xs[kExpertWaves][kFp8 ? kTileRows : 4];
+};
+constexpr int kScaleBlocks = 4;                  // blocks per load of scales
+
+// One object: between separate ones the compiler tracks which loads into LDS
+// might touch what is read, and waits for all in flight before every read.
+template <bool kFp8> struct TileShared {
+    TileStage<kFp8> ring[TileStage<kFp8>::kStages];
+    float ws[kExpertWaves][kScaleBlocks][kWaveCols];
+    float xs[kFp8 ? 2 : 1][kScaleBlocks][kTileRows];
 };
 
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, void* lds, int lane_offset, int offset)
 {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
-                                             lane_offset, offset, 0, 0);
-}
-
-__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, void* lds, int lane_offset, int offset)
-{
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4,
                                              lane_offset, offset, 0, 0);
 }
 
@@ -360,7 +363,7 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
     const float* __restrict__ ws, int outs, uint16_t* __restrict__ out, int n_groups)
 {
     using S = TileStage<kFp8>;
-    __shared__ __attribute__((aligned(16))) S ring[S::kStages];
+    __shared__ __attribute__((aligned(16))) TileShared<kFp8> lds;
     const int lane = threadIdx.x % kWave, m = lane % kTile, q = lane / kTile;
     const int wave = wave_uniform(threadIdx.x / kWave);
     // the column groups of one row tile on one XCD (they share its rows)
@@ -378,16 +381,16 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
 
     // codes: load j is operand tile j, lane i piece i % 4 of row i / 4 (past the
     // last output: other rows or 0, not stored)
-    __amdgpu_buffer_rsrc_t wr[kParts], sr[kParts];
+    __amdgpu_buffer_rsrc_t wr[kParts];
+    const int64_t n_base = min(n0, outs);
 #pragma unroll
     for (int h = 0; h < kParts; ++h) {
-        const int64_t r = min((int64_t)n0, (int64_t)outs) + (int64_t)h * outs;
+        const int64_t r = n_base + (int64_t)h * outs;
         wr[h] = buffer(w + (expert * wrows + r) * half_cols, (wrows - r) * half_cols);
-        sr[h] = buffer(ws + (expert * wrows + r) * blocks, (wrows - r) * blocks * 4);
     }
+    const __amdgpu_buffer_rsrc_t sr = buffer(ws + (expert * wrows + n_base) * blocks,
+                                             (wrows - n_base) * blocks * 4);
     const int wo = (lane / 4) * half_cols + ((lane % 4) ^ ((lane / 8) % 4)) * 16;
-    // scales: lane i that of weight row i of the wave; silu: lanes 32 .. 63 the up rows
-    const int so = (kSilu ? lane % kOuts : lane) * blocks * 4;
     // rows past the last are read as the last one; what they give is not stored
     const __amdgpu_buffer_rsrc_t xr = buffer(x + (int64_t)row0 * cols * (S::kRowBytes / kScaleBlock),
                                              (int64_t)count * cols * (S::kRowBytes / kScaleBlock));
@@ -401,7 +404,6 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
         const int piece = (lane % kPieces) ^ (r % kPieces);
         xo[p] = min(r, count - 1) * cols * (S::kRowBytes / kScaleBlock) + piece * 16;
     }
-    const int xso = min(lane, count - 1) * blocks * 4;
     auto load = [&](S& s, int b) {
         b = min(b, blocks - 1);                  // past the end: loads that nobody reads
 #pragma unroll
@@ -412,9 +414,38 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
 #pragma unroll
             for (int j = 0; j < kHalf; ++j)
                 load_lds16(wr[h], s.w[wave] + (h * kHalf + j) * 1024, wo, j * kTile * half_cols + b * 64);
-        if constexpr (!kSilu) load_lds4(sr[0], s.ws[wave], so, b * 4);
-        else load_lds4(sr[0], s.ws[wave], so + (lane / kOuts) * outs * blocks * 4, b * 4);
-        if constexpr (kFp8) load_lds4(xsr, s.xs[wave], xso, b * 4);
+    };
+    // Scales of blocks b .. b + 3: lane i that of weight row i of the wave (silu:
+    // lanes 32 .. 63 the up rows), lanes 0 .. 15 those of 16 of the fp8 rows.  The
+    // 4 blocks end at the row's last one at most: no load is partly past its
+    // buffer.
+    const int so = (kSilu ? lane % kOuts + lane / kOuts * outs : lane) * blocks * 4;
+    const int xso = min(wave * kTile + m, count - 1) * blocks * 4;
+    v4f wsv, xsv;
+    auto load_scales = [&](int b) {
+        if (blocks >= kScaleBlocks) {
+            const int bl = min(b, blocks - kScaleBlocks);
+            wsv = __builtin_bit_cast(v4f, load_b128(sr, so, bl * 4));
+            if constexpr (kFp8) xsv = __builtin_bit_cast(v4f, load_b128(xsr, xso, bl * 4));
+        } else {
+            v4i a, c;
+#pragma unroll
+            for (int i = 0; i < kScaleBlocks; ++i) {
+                a[i] = __builtin_amdgcn_raw_buffer_load_b32(sr, so, min(i, blocks - 1) * 4, 0);
+                c[i] = kFp8 ? __builtin_amdgcn_raw_buffer_load_b32(xsr, xso, min(i, blocks - 1) * 4, 0) : 0;
+            }
+            wsv = __builtin_bit_cast(v4f, a);
+            xsv = __builtin_bit_cast(v4f, c);
+        }
+    };
+    auto store_scales = [&](int b, int buf) {
+        const int skip = blocks >= kScaleBlocks ? b - min(b, blocks - kScaleBlocks) : 0;
+#pragma unroll
+        for (int i = 0; i < kScaleBlocks; ++i) {
+            if (i < skip) continue;
+            lds.ws[wave][i - skip][lane] = wsv[i];
+            if constexpr (kFp8) if (lane < kTile) lds.xs[buf][i - skip][wave * kTile + lane] = xsv[i];
+        }
     };
     v4f acc[kRowTiles][kColTiles];
 #pragma unroll
@@ -422,13 +453,13 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
 #pragma unroll
         for (int j = 0; j < kColTiles; ++j) acc[t][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto compute = [&](const S& s) {
+    auto compute = [&](const S& s, int buf, int i_block) {
         v4i wc[kColTiles];
         v4f sw[kColTiles];
 #pragma unroll
         for (int j = 0; j < kColTiles; ++j) {
             wc[j] = *(const v4i*)(s.w[wave] + j * 1024 + m * 64 + (q ^ ((m / 2) % 4)) * 16);
-            sw[j] = *(const v4f*)&s.ws[wave][j * kTile + q * 4];
+            sw[j] = *(const v4f*)&lds.ws[wave][i_block][j * kTile + q * 4];
         }
         if constexpr (kFp8) {
 #pragma unroll
@@ -438,7 +469,7 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
                 const v4i lo = *(const v4i*)(xrow + (q ^ (m % 8)) * 16);
                 const v4i hi = *(const v4i*)(xrow + ((4 + q) ^ (m % 8)) * 16);
                 const v8i xb = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                const float f = s.xs[wave][t * kTile + m];
+                const float f = lds.xs[buf][i_block][t * kTile + m];
                 v4f d[kColTiles];
 #pragma unroll
                 for (int j = 0; j < kColTiles; ++j) d[j] = block_product(wc[j], xb);
@@ -476,14 +507,22 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
     };
 
     constexpr int kAhead = S::kStages - 1;
+    load_scales(0);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(ring[i], i);
+    for (int i = 0; i < kAhead; ++i) load(lds.ring[i], i);
     int at = 0;
-    for (int b = 0; b < blocks; ++b) {
-        stage_barrier<(kAhead - 1) * S::kLoads>();
-        load(ring[at == 0 ? kAhead : at - 1], b + kAhead);      // the stage read last
-        compute(ring[at]);
-        at = at + 1 == S::kStages ? 0 : at + 1;
+    for (int b0 = 0; b0 < blocks; b0 += kScaleBlocks) {
+        const int buf = kFp8 ? (b0 / kScaleBlocks) % 2 : 0;
+        store_scales(b0, buf);
+#pragma unroll
+        for (int i = 0; i < kScaleBlocks; ++i) {
+            if (b0 + i >= blocks) break;
+            stage_barrier<(kAhead - 1) * S::kLoads>();
+            if (i == 0 && b0 + kScaleBlocks < blocks) load_scales(b0 + kScaleBlocks);
+            load(lds.ring[at == 0 ? kAhead : at - 1], b0 + i + kAhead);      // the stage read last
+            compute(lds.ring[at], buf, i);
+            at = at + 1 == S::kStages ? 0 : at + 1;
+        }
     }
     stage_barrier<0>();                          // nothing in flight into LDS when the wave ends
 #pragma unroll
