@@ -34,7 +34,6 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kTile = 16;
-constexpr int kExpertWaves = 4;
 constexpr int kMaxExpertCols = 1 << 23;      // 64 rows of bf16 within 31-bit offsets
 constexpr int64_t kMaxBuffer = 0x7FFFFFFF;
 
@@ -297,40 +296,43 @@ __global__ __launch_bounds__(kStreamWaves * kWave, kFp8 ? 4 : 3) void expert_str
     }
 }
 
-// Large batches: a workgroup computes up to 64 rows x 256 weight rows, 64 of
-// them per wave.  Codes and rows go from memory straight to LDS, a ring of
-// stages of one block each, kStages - 1 of them in flight; every wave loads its
-// own codes and a quarter of the rows, waits for its own loads of the oldest
-// stage and meets the others at one barrier per block.  Scales are loaded for
-// 4 blocks at a time (16 bytes of one row per lane: block by block they would
-// be one 4-byte piece of 64 lines) and kept in LDS transposed.
+// Large batches: a workgroup of 4 waves computes up to 64 rows x 256 weight
+// rows, 64 of them per wave.  Two blocks are a stage; the next stage is loaded
+// while one is computed, with one barrier per stage.  The codes go to the
+// registers of the one wave that needs them, the rows straight to LDS for all
+// four.  Two blocks, because their codes are 128 bytes of a row, one cache
+// line: stages of one block asked for every line twice, the second time while
+// it was on its way, and kept the cache waiting.  Scales are loaded for 4
+// blocks at a time (16 bytes of one row per lane: block by block they would be
+// one 4-byte piece of 64 lines) and kept in LDS transposed.
 //
-// A load of 16 bytes per lane covers whole rows of the block (codes: 16 rows x
-// 64 bytes; fp8 rows: 8 x 128; bf16: 4 x 256), and the 16-byte pieces of a row
-// are permuted (piece ^ row bits) so that 8 lanes reading one piece of 8
-// neighbouring rows meet 8 different banks.
-constexpr int kWaveCols = 64;                    // weight rows per wave: 4 operand tiles
-constexpr int kColTiles = kWaveCols / kTile;
+// A load into LDS, 16 bytes per lane, covers whole rows of a stage (fp8: 4 rows
+// x 256 bytes; bf16: 2 x 512), and the 16-byte pieces of a row are permuted
+// (piece ^ row) so that 8 lanes reading one piece of 8 neighbouring rows meet 8
+// different banks.
+constexpr int kTileWaves = 4;
 constexpr int kTileRows = 64;                    // rows per workgroup
 constexpr int kRowTiles = kTileRows / kTile;
+constexpr int kWaveCols = 64;                    // weight rows per wave: 4 operand tiles
+constexpr int kColTiles = kWaveCols / kTile;
+constexpr int kStageBlocks = 2;
+constexpr int kChunkTiles = 1;                   // row tiles that run together on an XCD
+constexpr int kScaleBlocks = 4;                  // blocks per load of scales
+static_assert(kScaleBlocks == 2 * kStageBlocks, "two stages, one in each set of registers");
 
 template <bool kFp8> struct TileStage {
-    static constexpr int kRowBytes = kScaleBlock * (kFp8 ? 1 : 2);
-    static constexpr int kRowsPerLoad = 1024 / kRowBytes;
-    static constexpr int kXLoads = kTileRows / kRowsPerLoad / kExpertWaves;      // per wave
-    static constexpr int kLoads = kXLoads + kColTiles;                           // per wave and stage
-    static constexpr int kStages = kFp8 ? 3 : 2;
-    uint8_t w[kExpertWaves][kWaveCols * kScaleBlock / 2];
+    static constexpr int kRowBytes = kStageBlocks * kScaleBlock * (kFp8 ? 1 : 2);
+    static constexpr int kPieces = kRowBytes / 16;
+    static constexpr int kXLoads = kTileRows * kRowBytes / 1024 / kTileWaves;          // per wave
     uint8_t x[kTileRows * kRowBytes];
 };
-constexpr int kScaleBlocks = 4;                  // blocks per load of scales
 
 // One object: between separate ones the compiler tracks which loads into LDS
 // might touch what is read, and waits for all in flight before every read.
 template <bool kFp8> struct TileShared {
-    TileStage<kFp8> ring[TileStage<kFp8>::kStages];
-    float ws[kExpertWaves][kScaleBlocks][kWaveCols];
-    float xs[kFp8 ? 2 : 1][kScaleBlocks][kTileRows];
+    TileStage<kFp8> stage[2];
+    float ws[kTileWaves][kScaleBlocks][kWaveCols];
+    float xs[kFp8 ? 2 : 1][kScaleBlocks][kFp8 ? kTileRows : 4];
 };
 
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, void* lds, int lane_offset, int offset)
@@ -339,25 +341,20 @@ __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, void* lds, 
                                              lane_offset, offset, 0, 0);
 }
 
-// Waits until at most kOutstanding of this wave's loads are in flight (they
-// complete in order) and its LDS reads are done, and meets the workgroup: then
-// the older loads of every wave are in LDS and what was read before may be
-// overwritten.  A workgroup fence in place of the empty asm statements, which
-// only keep the compiler from moving accesses across, would wait for every
-// load in flight into LDS.
-template <int kOutstanding>
+// Waits for this wave's loads into LDS and its LDS reads, and meets the
+// workgroup: then every wave's loads are there and what was read before may be
+// overwritten.  (The empty asm statements keep the compiler from moving
+// accesses across.)
 __device__ __forceinline__ void stage_barrier()
 {
-    static_assert(kOutstanding >= 0 && kOutstanding < 64, "vmcnt holds 6 bits");
     asm volatile("" ::: "memory");
-    // gfx9 encoding: vmcnt in bits 3:0 and 15:14, expcnt in 6:4 (not waited for), lgkmcnt 0 in 11:8
-    __builtin_amdgcn_s_waitcnt((kOutstanding & 15) | ((kOutstanding >> 4) << 14) | 0x70);
+    __builtin_amdgcn_s_waitcnt(0x70);            // gfx9 encoding: vmcnt 0, lgkmcnt 0, expcnt not waited for
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
 
 template <bool kFp8, bool kSilu>
-__global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
+__global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
     const uint8_t* __restrict__ x, const float* __restrict__ xs, int rows, int cols,
     const int32_t* __restrict__ off, int E, const uint8_t* __restrict__ w,
     const float* __restrict__ ws, int outs, uint16_t* __restrict__ out, int n_groups)
@@ -366,23 +363,23 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
     __shared__ __attribute__((aligned(16))) TileShared<kFp8> lds;
     const int lane = threadIdx.x % kWave, m = lane % kTile, q = lane / kTile;
     const int wave = wave_uniform(threadIdx.x / kWave);
-    // the column groups of one row tile on one XCD (they share its rows)
-    const int slot = blockIdx.x / kXcds;
-    const int tile = (slot / n_groups) * kXcds + blockIdx.x % kXcds;
+    // 4 row tiles at a time on one XCD, column group by column group: tiles of
+    // one expert share its codes in that XCD's L2, column groups the rows
+    const int slot = blockIdx.x / kXcds, chunk = slot / (kChunkTiles * n_groups);
+    const int in_chunk = slot % (kChunkTiles * n_groups), group = in_chunk / kChunkTiles;
+    const int tile = (chunk * kXcds + blockIdx.x % kXcds) * kChunkTiles + in_chunk % kChunkTiles;
     constexpr int kParts = kSilu ? 2 : 1;                      // gate and up rows
     constexpr int kOuts = kWaveCols / kParts;                  // outputs per wave
     constexpr int kHalf = kOuts / kTile;                       // operand tiles of a part
-    const int n0 = ((slot % n_groups) * kExpertWaves + wave) * kOuts;
+    const int n0 = (group * kTileWaves + wave) * kOuts;
     int expert, row0, count;
     if (!find_tile<kTileRows>(off, E, rows, tile, lane, expert, row0, count)) return;
-    const int live = (count + kTile - 1) / kTile;
     const int blocks = cols / kScaleBlock, half_cols = cols / 2;
     const int64_t wrows = (int64_t)outs * kParts;
 
-    // codes: load j is operand tile j, lane i piece i % 4 of row i / 4 (past the
-    // last output: other rows or 0, not stored)
-    __amdgpu_buffer_rsrc_t wr[kParts];
+    // (past the last output: other rows or 0, not stored)
     const int64_t n_base = min(n0, outs);
+    __amdgpu_buffer_rsrc_t wr[kParts];
 #pragma unroll
     for (int h = 0; h < kParts; ++h) {
         const int64_t r = n_base + (int64_t)h * outs;
@@ -390,30 +387,36 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
     }
     const __amdgpu_buffer_rsrc_t sr = buffer(ws + (expert * wrows + n_base) * blocks,
                                              (wrows - n_base) * blocks * 4);
-    const int wo = (lane / 4) * half_cols + ((lane % 4) ^ ((lane / 8) % 4)) * 16;
-    // rows past the last are read as the last one; what they give is not stored
-    const __amdgpu_buffer_rsrc_t xr = buffer(x + (int64_t)row0 * cols * (S::kRowBytes / kScaleBlock),
-                                             (int64_t)count * cols * (S::kRowBytes / kScaleBlock));
+    const int wo = m * half_cols + q * 16;
+    // rows past the last are past the buffer: not fetched (read as another row
+    // they would ask for lines already on their way); what they give is not stored
+    constexpr int kElem = kFp8 ? 1 : 2;
+    const __amdgpu_buffer_rsrc_t xr = buffer(x + (int64_t)row0 * cols * kElem, (int64_t)count * cols * kElem);
     const __amdgpu_buffer_rsrc_t xsr = buffer(kFp8 ? xs + (int64_t)row0 * blocks : nullptr,
                                               kFp8 ? (int64_t)count * blocks * 4 : 0);
+    // load p of a wave is load p * 4 + wave of the stage: few rows are shared out
+    constexpr int kLoadRows = kWave / S::kPieces;
     int xo[S::kXLoads];
 #pragma unroll
     for (int p = 0; p < S::kXLoads; ++p) {
-        constexpr int kPieces = S::kRowBytes / 16;
-        const int r = (wave * S::kXLoads + p) * S::kRowsPerLoad + lane / kPieces;
-        const int piece = (lane % kPieces) ^ (r % kPieces);
-        xo[p] = min(r, count - 1) * cols * (S::kRowBytes / kScaleBlock) + piece * 16;
+        const int r = (p * kTileWaves + wave) * kLoadRows + lane / S::kPieces;
+        const int piece = (lane % S::kPieces) ^ (r % kTile);
+        xo[p] = r * cols * kElem + piece * 16;
     }
-    auto load = [&](S& s, int b) {
-        b = min(b, blocks - 1);                  // past the end: loads that nobody reads
+    // blocks b and b + 1 (b + 1 past the last: the next row or 0, not used)
+    struct Codes { v4i w[kStageBlocks][kColTiles]; };
+    auto load = [&](Codes& c, S& s, int b) {
 #pragma unroll
         for (int p = 0; p < S::kXLoads; ++p)
-            load_lds16(xr, s.x + (wave * S::kXLoads + p) * 1024, xo[p], b * S::kRowBytes);
+            if ((p * kTileWaves + wave) * kLoadRows < count)
+                load_lds16(xr, s.x + (p * kTileWaves + wave) * 1024, xo[p], b * kScaleBlock * kElem);
 #pragma unroll
         for (int h = 0; h < kParts; ++h)
 #pragma unroll
             for (int j = 0; j < kHalf; ++j)
-                load_lds16(wr[h], s.w[wave] + (h * kHalf + j) * 1024, wo, j * kTile * half_cols + b * 64);
+#pragma unroll
+                for (int u = 0; u < kStageBlocks; ++u)
+                    c.w[u][h * kHalf + j] = load_b128(wr[h], wo, j * kTile * half_cols + (b + u) * 64);
     };
     // Scales of blocks b .. b + 3: lane i that of weight row i of the wave (silu:
     // lanes 32 .. 63 the up rows), lanes 0 .. 15 those of 16 of the fp8 rows.  The
@@ -447,100 +450,118 @@ __global__ __launch_bounds__(kExpertWaves * kWave, 2) void expert_tile_kernel(
             if constexpr (kFp8) if (lane < kTile) lds.xs[buf][i - skip][wave * kTile + lane] = xsv[i];
         }
     };
-    v4f acc[kRowTiles][kColTiles];
-#pragma unroll
-    for (int t = 0; t < kRowTiles; ++t)
-#pragma unroll
-        for (int j = 0; j < kColTiles; ++j) acc[t][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-
-    auto compute = [&](const S& s, int buf, int i_block) {
-        v4i wc[kColTiles];
-        v4f sw[kColTiles];
-#pragma unroll
-        for (int j = 0; j < kColTiles; ++j) {
-            wc[j] = *(const v4i*)(s.w[wave] + j * 1024 + m * 64 + (q ^ ((m / 2) % 4)) * 16);
-            sw[j] = *(const v4f*)&lds.ws[wave][i_block][j * kTile + q * 4];
-        }
+    // Block u of a stage, block i of the scales, kLive groups of 16 rows.
+    auto compute = [&](auto kLive, auto& acc, const Codes& c, const S& s, int u, int buf, int i) {
+        constexpr int kN = decltype(kLive)::value;
+        auto x_at = [&](int t, int piece) {
+            return *(const v4i*)(s.x + (t * kTile + m) * S::kRowBytes + (piece ^ m) * 16);
+        };
         if constexpr (kFp8) {
+            // the products of a group are scaled and added while the next group's run
+            v4f sw[kColTiles], d[2][kColTiles];
+            float f[3];                          // of the group before, this one and the next
+            v8i xv[2];
 #pragma unroll
-            for (int t = 0; t < kRowTiles; ++t) {
-                if (t >= live) break;
-                const uint8_t* const xrow = s.x + (t * kTile + m) * 128;
-                const v4i lo = *(const v4i*)(xrow + (q ^ (m % 8)) * 16);
-                const v4i hi = *(const v4i*)(xrow + ((4 + q) ^ (m % 8)) * 16);
-                const v8i xb = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                const float f = lds.xs[buf][i_block][t * kTile + m];
-                v4f d[kColTiles];
+            for (int j = 0; j < kColTiles; ++j) sw[j] = *(const v4f*)&lds.ws[wave][i][j * kTile + q * 4];
+            auto get = [&](int t) {
+                const v4i lo = x_at(t, u * 8 + q), hi = x_at(t, u * 8 + 4 + q);
+                xv[t % 2] = (v8i){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                f[t % 3] = lds.xs[buf][i][t * kTile + m];
+            };
+            auto add = [&](int t, int j) {
 #pragma unroll
-                for (int j = 0; j < kColTiles; ++j) d[j] = block_product(wc[j], xb);
+                for (int k = 0; k < 4; ++k)
+                    acc[t][j][k] = __builtin_fmaf(d[t % 2][j][k], sw[j][k] * f[t % 3], acc[t][j][k]);
+            };
+            get(0);
 #pragma unroll
-                for (int j = 0; j < kColTiles; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[t][j][i] = __builtin_fmaf(d[j][i], sw[j][i] * f, acc[t][j][i]);
-            }
-        } else {
-            v8bf wb[kColTiles][4];
-#pragma unroll
-            for (int j = 0; j < kColTiles; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) wb[j][i] = bf16x8_of_codes((uint32_t)wc[j][i]);
-#pragma unroll
-            for (int t = 0; t < kRowTiles; ++t) {
-                if (t >= live) break;
-                v8bf xb[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    xb[i] = *(const v8bf*)(s.x + (t * kTile + m) * 256 + ((q * 4 + i) ^ m) * 16);
+            for (int t = 0; t < kN; ++t) {
+                if (t + 1 < kN) get(t + 1);
 #pragma unroll
                 for (int j = 0; j < kColTiles; ++j) {
-                    v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][i], xb[i], d, 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[t][j][i] = __builtin_fmaf(d[i], sw[j][i], acc[t][j][i]);
+                    d[t % 2][j] = block_product(c.w[u][j], xv[t % 2]);
+                    if (t > 0) add(t - 1, j);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < kColTiles; ++j) add(kN - 1, j);
+        } else {
+            v8bf xv[kN][4];
+#pragma unroll
+            for (int t = 0; t < kN; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) xv[t][k] = __builtin_bit_cast(v8bf, x_at(t, u * 16 + q * 4 + k));
+#pragma unroll
+            for (int j = 0; j < kColTiles; ++j) {
+                const v4f sw = *(const v4f*)&lds.ws[wave][i][j * kTile + q * 4];
+                v8bf wb[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) wb[k] = bf16x8_of_codes((uint32_t)c.w[u][j][k]);
+                v4f d[kN];
+#pragma unroll
+                for (int t = 0; t < kN; ++t) d[t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int t = 0; t < kN; ++t)
+                        d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[k], xv[t][k], d[t], 0, 0, 0);
+#pragma unroll
+                for (int t = 0; t < kN; ++t)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[t][j][k] = __builtin_fmaf(d[t][k], sw[k], acc[t][j][k]);
             }
         }
     };
-
-    constexpr int kAhead = S::kStages - 1;
-    load_scales(0);
+    // The whole product of kLive groups of 16 rows: a variant each, so that the
+    // sums stay in their registers.
+    auto run = [&](auto kLive) {
+        constexpr int kN = decltype(kLive)::value;
+        v4f acc[kN][kColTiles];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(lds.ring[i], i);
-    int at = 0;
-    for (int b0 = 0; b0 < blocks; b0 += kScaleBlocks) {
-        const int buf = kFp8 ? (b0 / kScaleBlocks) % 2 : 0;
-        store_scales(b0, buf);
+        for (int t = 0; t < kN; ++t)
 #pragma unroll
-        for (int i = 0; i < kScaleBlocks; ++i) {
-            if (b0 + i >= blocks) break;
-            stage_barrier<(kAhead - 1) * S::kLoads>();
-            if (i == 0 && b0 + kScaleBlocks < blocks) load_scales(b0 + kScaleBlocks);
-            load(lds.ring[at == 0 ? kAhead : at - 1], b0 + i + kAhead);      // the stage read last
-            compute(lds.ring[at], buf, i);
-            at = at + 1 == S::kStages ? 0 : at + 1;
+            for (int j = 0; j < kColTiles; ++j) acc[t][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+        Codes codes[2];
+        load_scales(0);
+        load(codes[0], lds.stage[0], 0);
+        for (int b0 = 0; b0 < blocks; b0 += kScaleBlocks) {
+            const int buf = kFp8 ? (b0 / kScaleBlocks) % 2 : 0;
+            store_scales(b0, buf);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int b = b0 + i * kStageBlocks;
+                if (b >= blocks) break;
+                stage_barrier();
+                if (i == 0 && b0 + kScaleBlocks < blocks) load_scales(b0 + kScaleBlocks);
+                if (b + kStageBlocks < blocks) load(codes[1 - i], lds.stage[1 - i], b + kStageBlocks);
+                compute(kLive, acc, codes[i], lds.stage[i], 0, buf, i * kStageBlocks);
+                if (b + 1 < blocks) compute(kLive, acc, codes[i], lds.stage[i], 1, buf, i * kStageBlocks + 1);
+            }
         }
-    }
-    stage_barrier<0>();                          // nothing in flight into LDS when the wave ends
 #pragma unroll
-    for (int t = 0; t < kRowTiles; ++t) {
-        const int r = t * kTile + m;
-        if (r >= count) continue;
-        uint16_t* const orow = out + (int64_t)(row0 + r) * outs;
+        for (int t = 0; t < kN; ++t) {
+            const int r = t * kTile + m;
+            if (r >= count) continue;
+            uint16_t* const orow = out + (int64_t)(row0 + r) * outs;
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
-            const int n = n0 + j * kTile + q * 4;
-            if (n >= outs) continue;
-            float v[4];
+            for (int j = 0; j < kHalf; ++j) {
+                const int n = n0 + j * kTile + q * 4;
+                if (n >= outs) continue;
+                float v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[i] = kSilu ? silu_mul(acc[t][j][i], acc[t][(j + kHalf) % kColTiles][i]) : acc[t][j][i];
-            store8<false>(orow + n, make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])));
+                for (int k = 0; k < 4; ++k)
+                    v[k] = kSilu ? silu_mul(acc[t][j][k], acc[t][(j + kHalf) % kColTiles][k]) : acc[t][j][k];
+                store8<false>(orow + n, make_uint2(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])));
+            }
         }
-    }
+    };
+    const int live = (count + kTile - 1) / kTile;
+    if (live == 1) run(std::integral_constant<int, 1>());
+    else if (live == 2) run(std::integral_constant<int, 2>());
+    else if (live == 3) run(std::integral_constant<int, 3>());
+    else run(std::integral_constant<int, kRowTiles>());
 }
 
 }  // namespace
@@ -557,11 +578,17 @@ int64_t max_tiles(int rows, int E, int height)
 // Few rows per expert: the kernel that streams the weights; more: the tiles.
 bool expert_large(int rows, int E) { return rows > 8 * (int64_t)E; }
 
+int tile_groups(bool silu, int outs)
+{
+    const int per = kTileWaves * (silu ? kWaveCols / 2 : kWaveCols);
+    return (int)(((int64_t)outs + per - 1) / per);
+}
+
 int64_t tile_blocks(bool silu, int rows, int outs, int E)
 {
-    const int per = kExpertWaves * (silu ? kWaveCols / 2 : kWaveCols);
-    const int64_t groups = ((int64_t)outs + per - 1) / per;
-    return (max_tiles(rows, E, kTileRows) + kXcds - 1) / kXcds * kXcds * groups;
+    const int64_t tiles = max_tiles(rows, E, kTileRows);
+    constexpr int kRound = kXcds * kChunkTiles;
+    return (tiles + kRound - 1) / kRound * kRound * tile_groups(silu, outs);
 }
 
 int stream_groups(bool silu, int outs)
@@ -589,11 +616,11 @@ bool expert_launch_ok(bool silu, int rows, int cols, int outs, int E)
 {
     // offsets within a tile are 32-bit; a grid dimension holds fewer than 2^32 threads
     if (cols > kMaxExpertCols || outs > (1 << 29)) return false;
-    static_assert(kExpertWaves == kStreamWaves, "both kernels launch the same workgroups");
     if (silu && (int64_t)outs * cols >= ((int64_t)1 << 36)) return false;
-    const int64_t blocks = expert_large(rows, E) ? tile_blocks(silu, rows, outs, E)
-                                                 : stream_blocks(silu, rows, cols, outs, E);
-    return blocks * kExpertWaves * kWave < ((int64_t)1 << 32);
+    const int64_t threads = expert_large(rows, E)
+        ? tile_blocks(silu, rows, outs, E) * kTileWaves * kWave
+        : stream_blocks(silu, rows, cols, outs, E) * kStreamWaves * kWave;
+    return threads < ((int64_t)1 << 32);
 }
 
 hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int rows, int cols,
@@ -601,14 +628,12 @@ hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int row
                          const float* w_scales, int outs, bool silu, uint16_t* out,
                          hipStream_t stream)
 {
-    const dim3 block(kExpertWaves * kWave);
     if (expert_large(rows, E)) {
-        const int per = kExpertWaves * (silu ? kWaveCols / 2 : kWaveCols);
-        const int groups = (outs + per - 1) / per;
         const dim3 grid((unsigned)tile_blocks(silu, rows, outs, E));
         auto go = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, grid, block, 0, stream, (const uint8_t*)x, x_scales, rows,
-                               cols, expert_offset, E, w, w_scales, outs, out, groups);
+            hipLaunchKernelGGL(kernel, grid, dim3(kTileWaves * kWave), 0, stream, (const uint8_t*)x,
+                               x_scales, rows, cols, expert_offset, E, w, w_scales, outs, out,
+                               tile_groups(silu, outs));
         };
         if (fp8) silu ? go(expert_tile_kernel<true, true>) : go(expert_tile_kernel<true, false>);
         else silu ? go(expert_tile_kernel<false, true>) : go(expert_tile_kernel<false, false>);
@@ -618,8 +643,8 @@ hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int row
     const int groups = stream_groups(silu, outs), teams = kStreamWaves / split;
     const dim3 grid((unsigned)stream_blocks(silu, rows, cols, outs, E));
     auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, block, 0, stream, (const uint8_t*)x, x_scales, rows, cols,
-                           expert_offset, E, w, w_scales, outs, out, groups, (groups + teams - 1) / teams);
+        hipLaunchKernelGGL(kernel, grid, dim3(kStreamWaves * kWave), 0, stream, (const uint8_t*)x,
+                           x_scales, rows, cols, expert_offset, E, w, w_scales, outs, out, groups, (groups + teams - 1) / teams);
     };
     auto pick = [&](auto sp) {
         constexpr int kS = decltype(sp)::value;
