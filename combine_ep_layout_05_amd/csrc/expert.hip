@@ -298,57 +298,57 @@ __global__ __launch_bounds__(kStreamWaves * kWave, kFp8 ? 4 : 3) void expert_str
 
 // Large batches: a workgroup of 4 waves computes up to 64 rows x 256 weight
 // rows, 64 of them per wave.  Two blocks are a stage; the next stage is loaded
-// while one is computed, with one barrier per stage.  The codes go to the
-// registers of the one wave that needs them, the rows straight to LDS for all
-// four.  Two blocks, because their codes are 128 bytes of a row, one cache
-// line: stages of one block asked for every line twice, the second time while
-// it was on its way, and kept the cache waiting.  Scales are loaded for 4
-// blocks at a time (16 bytes of one row per lane: block by block they would be
-// one 4-byte piece of 64 lines) and kept in LDS transposed.
+// while one is computed.  The rows go straight to LDS for all four waves.  The
+// codes go through the registers of the wave that needs them to its own part
+// of LDS: a load covers 128 bytes, a cache line, of each of 8 rows, where the
+// operand has 64 bytes of 16 (loaded like that every line is asked for twice,
+// and the address unit, 16 rows an instruction, bounds the kernel).  Scales are
+// loaded for 4 blocks at a time (16 bytes of one row per lane) and kept in LDS
+// transposed.
 //
-// A load into LDS, 16 bytes per lane, covers whole rows of a stage (fp8: 4 rows
-// x 256 bytes; bf16: 2 x 512), and the 16-byte pieces of a row are permuted
-// (piece ^ row) so that 8 lanes reading one piece of 8 neighbouring rows meet 8
-// different banks.
+// The 16-byte pieces of a row in LDS are permuted (piece ^ row) so that 8
+// lanes reading one piece of 8 neighbouring rows meet 8 different banks.
 constexpr int kTileWaves = 4;
 constexpr int kTileRows = 64;                    // rows per workgroup
 constexpr int kRowTiles = kTileRows / kTile;
 constexpr int kWaveCols = 64;                    // weight rows per wave: 4 operand tiles
 constexpr int kColTiles = kWaveCols / kTile;
 constexpr int kStageBlocks = 2;
-constexpr int kChunkTiles = 1;                   // row tiles that run together on an XCD
+constexpr int kCodeLoads = kWaveCols * kStageBlocks * 64 / 1024;                       // per wave
+constexpr int kChunkTiles = 4;                   // row tiles that run together on an XCD
 constexpr int kScaleBlocks = 4;                  // blocks per load of scales
-static_assert(kScaleBlocks == 2 * kStageBlocks, "two stages, one in each set of registers");
 
-template <bool kFp8> struct TileStage {
-    static constexpr int kRowBytes = kStageBlocks * kScaleBlock * (kFp8 ? 1 : 2);
-    static constexpr int kPieces = kRowBytes / 16;
-    static constexpr int kXLoads = kTileRows * kRowBytes / 1024 / kTileWaves;          // per wave
-    uint8_t x[kTileRows * kRowBytes];
-};
-
-// One object: between separate ones the compiler tracks which loads into LDS
-// might touch what is read, and waits for all in flight before every read.
 template <bool kFp8> struct TileShared {
-    TileStage<kFp8> stage[2];
+    // rows: fp8 a stage of 2 blocks (256 bytes of a row), bf16 of one (also 256)
+    static constexpr int kRowBytes = 256;
+    static constexpr int kXBlocks = kFp8 ? 2 : 1;
+    static constexpr int kXLoads = kTileRows * kRowBytes / 1024 / kTileWaves;          // per wave
+    uint8_t x[2][kTileRows * kRowBytes];
+    uint8_t w[kTileWaves][kWaveCols * kStageBlocks * 64];
     float ws[kTileWaves][kScaleBlocks][kWaveCols];
     float xs[kFp8 ? 2 : 1][kScaleBlocks][kFp8 ? kTileRows : 4];
 };
 
+// 16 bytes per lane straight to LDS, lane after lane.  All of a kernel's LDS is
+// one object: between separate ones the compiler tracks which of these loads
+// might touch what is read, and waits for all in flight before every read.
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, void* lds, int lane_offset, int offset)
 {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
                                              lane_offset, offset, 0, 0);
 }
 
-// Waits for this wave's loads into LDS and its LDS reads, and meets the
-// workgroup: then every wave's loads are there and what was read before may be
+// Waits until at most kOutstanding of this wave's loads are in flight (they
+// complete in order) and its LDS accesses are done, and meets the workgroup:
+// then every wave's older loads are in LDS and what was read before may be
 // overwritten.  (The empty asm statements keep the compiler from moving
-// accesses across.)
+// accesses across; a fence would wait for every load in flight into LDS.)
+template <int kOutstanding>
 __device__ __forceinline__ void stage_barrier()
 {
+    static_assert(kOutstanding >= 0 && kOutstanding < 16, "one field of the encoding is used");
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x70);            // gfx9 encoding: vmcnt 0, lgkmcnt 0, expcnt not waited for
+    __builtin_amdgcn_s_waitcnt(kOutstanding | 0x70);   // gfx9 encoding: vmcnt, lgkmcnt 0, expcnt not waited for
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -359,8 +359,8 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
     const int32_t* __restrict__ off, int E, const uint8_t* __restrict__ w,
     const float* __restrict__ ws, int outs, uint16_t* __restrict__ out, int n_groups)
 {
-    using S = TileStage<kFp8>;
-    __shared__ __attribute__((aligned(16))) TileShared<kFp8> lds;
+    using S = TileShared<kFp8>;
+    __shared__ __attribute__((aligned(16))) S lds;   // one object: see load_lds16
     const int lane = threadIdx.x % kWave, m = lane % kTile, q = lane / kTile;
     const int wave = wave_uniform(threadIdx.x / kWave);
     // 4 row tiles at a time on one XCD, column group by column group: tiles of
@@ -387,36 +387,40 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
     }
     const __amdgpu_buffer_rsrc_t sr = buffer(ws + (expert * wrows + n_base) * blocks,
                                              (wrows - n_base) * blocks * 4);
-    const int wo = m * half_cols + q * 16;
+    const int wo = (lane / 8) * half_cols + (lane % 8) * 16;
     // rows past the last are past the buffer: not fetched (read as another row
     // they would ask for lines already on their way); what they give is not stored
     constexpr int kElem = kFp8 ? 1 : 2;
     const __amdgpu_buffer_rsrc_t xr = buffer(x + (int64_t)row0 * cols * kElem, (int64_t)count * cols * kElem);
     const __amdgpu_buffer_rsrc_t xsr = buffer(kFp8 ? xs + (int64_t)row0 * blocks : nullptr,
                                               kFp8 ? (int64_t)count * blocks * 4 : 0);
-    // load p of a wave is load p * 4 + wave of the stage: few rows are shared out
-    constexpr int kLoadRows = kWave / S::kPieces;
+    // load p of a wave is load p * 4 + wave of the stage: few rows are shared
+    // out; lane i piece i % 16 of row i / 16 of the load
     int xo[S::kXLoads];
 #pragma unroll
     for (int p = 0; p < S::kXLoads; ++p) {
-        const int r = (p * kTileWaves + wave) * kLoadRows + lane / S::kPieces;
-        const int piece = (lane % S::kPieces) ^ (r % kTile);
-        xo[p] = r * cols * kElem + piece * 16;
+        const int r = (p * kTileWaves + wave) * 4 + q;
+        xo[p] = r * cols * kElem + ((m ^ (r % kTile)) * 16);
     }
-    // blocks b and b + 1 (b + 1 past the last: the next row or 0, not used)
-    struct Codes { v4i w[kStageBlocks][kColTiles]; };
-    auto load = [&](Codes& c, S& s, int b) {
+    // (past the last block: the next row or 0, not used)
+    auto load_x = [&](int buf, int b) {
 #pragma unroll
         for (int p = 0; p < S::kXLoads; ++p)
-            if ((p * kTileWaves + wave) * kLoadRows < count)
-                load_lds16(xr, s.x + (p * kTileWaves + wave) * 1024, xo[p], b * kScaleBlock * kElem);
+            if ((p * kTileWaves + wave) * 4 < count)
+                load_lds16(xr, lds.x[buf] + (p * kTileWaves + wave) * 1024, xo[p], b * kScaleBlock * kElem);
+    };
+    // codes of blocks b and b + 1: lane i piece i % 8 of row i / 8 of the load
+    v4i cv[kCodeLoads];
+    auto load_codes = [&](int b) {
+        constexpr int kPer = kCodeLoads / kParts;
 #pragma unroll
-        for (int h = 0; h < kParts; ++h)
+        for (int p = 0; p < kCodeLoads; ++p)
+            cv[p] = load_b128(wr[p / kPer], wo, (p % kPer) * 8 * half_cols + b * 64);
+    };
+    auto store_codes = [&]() {
 #pragma unroll
-            for (int j = 0; j < kHalf; ++j)
-#pragma unroll
-                for (int u = 0; u < kStageBlocks; ++u)
-                    c.w[u][h * kHalf + j] = load_b128(wr[h], wo, j * kTile * half_cols + (b + u) * 64);
+        for (int p = 0; p < kCodeLoads; ++p)
+            *(v4i*)(lds.w[wave] + p * 1024 + (lane / 8) * 128 + ((lane % 8) ^ (lane / 8)) * 16) = cv[p];
     };
     // Scales of blocks b .. b + 3: lane i that of weight row i of the wave (silu:
     // lanes 32 .. 63 the up rows), lanes 0 .. 15 those of 16 of the fp8 rows.  The
@@ -451,11 +455,15 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
         }
     };
     // Block u of a stage, block i of the scales, kLive groups of 16 rows.
-    auto compute = [&](auto kLive, auto& acc, const Codes& c, const S& s, int u, int buf, int i) {
+    auto compute = [&](auto kLive, auto& acc, const uint8_t* sx, int u, int buf, int i) {
         constexpr int kN = decltype(kLive)::value;
         auto x_at = [&](int t, int piece) {
-            return *(const v4i*)(s.x + (t * kTile + m) * S::kRowBytes + (piece ^ m) * 16);
+            return *(const v4i*)(sx + (t * kTile + m) * S::kRowBytes + (piece ^ m) * 16);
         };
+        v4i wc[kColTiles];
+#pragma unroll
+        for (int j = 0; j < kColTiles; ++j)
+            wc[j] = *(const v4i*)(lds.w[wave] + (j * kTile + m) * 128 + ((u * 4 + q) ^ (m % 8)) * 16);
         if constexpr (kFp8) {
             // the products of a group are scaled and added while the next group's run
             v4f sw[kColTiles], d[2][kColTiles];
@@ -479,7 +487,7 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
                 if (t + 1 < kN) get(t + 1);
 #pragma unroll
                 for (int j = 0; j < kColTiles; ++j) {
-                    d[t % 2][j] = block_product(c.w[u][j], xv[t % 2]);
+                    d[t % 2][j] = block_product(wc[j], xv[t % 2]);
                     if (t > 0) add(t - 1, j);
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -491,13 +499,13 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
 #pragma unroll
             for (int t = 0; t < kN; ++t)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) xv[t][k] = __builtin_bit_cast(v8bf, x_at(t, u * 16 + q * 4 + k));
+                for (int k = 0; k < 4; ++k) xv[t][k] = __builtin_bit_cast(v8bf, x_at(t, q * 4 + k));
 #pragma unroll
             for (int j = 0; j < kColTiles; ++j) {
                 const v4f sw = *(const v4f*)&lds.ws[wave][i][j * kTile + q * 4];
                 v8bf wb[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) wb[k] = bf16x8_of_codes((uint32_t)c.w[u][j][k]);
+                for (int k = 0; k < 4; ++k) wb[k] = bf16x8_of_codes((uint32_t)wc[j][k]);
                 v4f d[kN];
 #pragma unroll
                 for (int t = 0; t < kN; ++t) d[t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
@@ -523,21 +531,36 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
         for (int t = 0; t < kN; ++t)
 #pragma unroll
             for (int j = 0; j < kColTiles; ++j) acc[t][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-        Codes codes[2];
         load_scales(0);
-        load(codes[0], lds.stage[0], 0);
+        load_x(0, 0);
+        load_codes(0);
         for (int b0 = 0; b0 < blocks; b0 += kScaleBlocks) {
             const int buf = kFp8 ? (b0 / kScaleBlocks) % 2 : 0;
             store_scales(b0, buf);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int b = b0 + i * kStageBlocks;
+            for (int i = 0; i < kScaleBlocks; i += kStageBlocks) {
+                const int b = b0 + i;
                 if (b >= blocks) break;
-                stage_barrier();
+                const bool more = b + kStageBlocks < blocks;
+                store_codes();
+                stage_barrier<0>();
                 if (i == 0 && b0 + kScaleBlocks < blocks) load_scales(b0 + kScaleBlocks);
-                if (b + kStageBlocks < blocks) load(codes[1 - i], lds.stage[1 - i], b + kStageBlocks);
-                compute(kLive, acc, codes[i], lds.stage[i], 0, buf, i * kStageBlocks);
-                if (b + 1 < blocks) compute(kLive, acc, codes[i], lds.stage[i], 1, buf, i * kStageBlocks + 1);
+                if constexpr (kFp8) {
+                    const int cur = i / kStageBlocks;
+                    if (more) { load_x(1 - cur, b + kStageBlocks); load_codes(b + kStageBlocks); }
+                    compute(kLive, acc, lds.x[cur], 0, buf, i);
+                    if (b + 1 < blocks) compute(kLive, acc, lds.x[cur], 1, buf, i + 1);
+                } else {
+                    if (b + 1 < blocks) load_x(1, b + 1);
+                    if (more) load_codes(b + kStageBlocks);
+                    compute(kLive, acc, lds.x[0], 0, buf, i);
+                    if (b + 1 < blocks) {
+                        // the rows of block b + 1; the codes after them may still be in flight
+                        if (more) stage_barrier<kCodeLoads>(); else stage_barrier<0>();
+                        if (more) load_x(0, b + kStageBlocks);
+                        compute(kLive, acc, lds.x[1], 1, buf, i + 1);
+                    }
+                }
             }
         }
 #pragma unroll
