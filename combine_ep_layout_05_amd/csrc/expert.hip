@@ -122,9 +122,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, int64
                                              (int)(bytes < kMaxBuffer ? bytes : kMaxBuffer), 0x00020000);
 }
 
+template <bool kOnce = false>              // kOnce: nontemporal
 __device__ __forceinline__ v4i load_b128(__amdgpu_buffer_rsrc_t r, int lane_offset, int offset)
 {
-    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, lane_offset, offset, 0));
+    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, lane_offset, offset, kOnce ? 2 : 0));
 }
 
 // Few rows per expert: the weights are read once and bound the time, so the
@@ -376,6 +377,8 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
     if (!find_tile<kTileRows>(off, E, rows, tile, lane, expert, row0, count)) return;
     const int blocks = cols / kScaleBlock, half_cols = cols / 2;
     const int64_t wrows = (int64_t)outs * kParts;
+    // the expert's only tile: nobody else wants its codes in the L2
+    const bool alone = off[expert + 1] - off[expert] <= kTileRows;
 
     // (past the last output: other rows or 0, not stored)
     const int64_t n_base = min(n0, outs);
@@ -413,9 +416,15 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
     v4i cv[kCodeLoads];
     auto load_codes = [&](int b) {
         constexpr int kPer = kCodeLoads / kParts;
+        if (alone) {
 #pragma unroll
-        for (int p = 0; p < kCodeLoads; ++p)
-            cv[p] = load_b128(wr[p / kPer], wo, (p % kPer) * 8 * half_cols + b * 64);
+            for (int p = 0; p < kCodeLoads; ++p)
+                cv[p] = load_b128<true>(wr[p / kPer], wo, (p % kPer) * 8 * half_cols + b * 64);
+        } else {
+#pragma unroll
+            for (int p = 0; p < kCodeLoads; ++p)
+                cv[p] = load_b128(wr[p / kPer], wo, (p % kPer) * 8 * half_cols + b * 64);
+        }
     };
     auto store_codes = [&]() {
 #pragma unroll
@@ -598,13 +607,25 @@ int64_t max_tiles(int rows, int E, int height)
     return (int64_t)rows / height + (rows < E ? rows : E);
 }
 
-// Few rows per expert: the kernel that streams the weights; more: the tiles.
-bool expert_large(int rows, int E) { return rows > 8 * (int64_t)E; }
-
 int tile_groups(bool silu, int outs)
 {
     const int per = kTileWaves * (silu ? kWaveCols / 2 : kWaveCols);
     return (int)(((int64_t)outs + per - 1) / per);
+}
+
+// Which kernel a batch runs, by its rows per expert (the routing is on the
+// device, so by their average).  Measured on MI355X, streaming against tiles,
+// gate and up products of 4096 columns:
+//   32 experts x 2 x 2048 weight rows (512 workgroups of tiles), fp8 rows: 40 /
+//   46 us at 1 row per expert, 52 / 47 at 2, 58 / 50 at 8, 116 / 55 at 32;
+//   bf16: 60 / 66 at 4, 69 / 67 at 8, 95 / 72 at 16;
+//   8 experts (128 workgroups, half the CUs), fp8: 17 / 37 at 8, 32 / 44 at 32,
+//   55 / 52 at 64; bf16: 42 / 65 at 32, 71 / 76 at 64.
+// (bf16 tiles take longer: the conversion of the codes is shared by few rows.)
+bool expert_large(bool fp8, bool silu, int rows, int outs, int E)
+{
+    const bool fill = (int64_t)E * tile_groups(silu, outs) >= 2 * kCUs;
+    return rows >= (fill ? (fp8 ? 2 : 8) : 64) * (int64_t)E;
 }
 
 int64_t tile_blocks(bool silu, int rows, int outs, int E)
@@ -620,7 +641,10 @@ int stream_groups(bool silu, int outs)
     return (int)(((int64_t)outs + per - 1) / per);
 }
 
-// Waves that share a group in the streaming kernel.
+// Waves that share a group in the streaming kernel: all four when the columns
+// are many or there are few groups, else one.  Measured (1 / 4 waves): 128
+// tokens, 288 experts, 2048 columns 406 / 470 us, 7168 columns 802 / 750 us; one
+// token, 8 experts x 6144 columns 32 / 21 us.
 int stream_split(bool silu, int rows, int cols, int outs, int E)
 {
     const bool many = max_tiles(rows, E, kTile) * stream_groups(silu, outs) >= kStreamManyGroups;
@@ -635,12 +659,12 @@ int64_t stream_blocks(bool silu, int rows, int cols, int outs, int E)
 
 }  // namespace
 
-bool expert_launch_ok(bool silu, int rows, int cols, int outs, int E)
+bool expert_launch_ok(bool fp8, bool silu, int rows, int cols, int outs, int E)
 {
     // offsets within a tile are 32-bit; a grid dimension holds fewer than 2^32 threads
     if (cols > kMaxExpertCols || outs > (1 << 29)) return false;
     if (silu && (int64_t)outs * cols >= ((int64_t)1 << 36)) return false;
-    const int64_t threads = expert_large(rows, E)
+    const int64_t threads = expert_large(fp8, silu, rows, outs, E)
         ? tile_blocks(silu, rows, outs, E) * kTileWaves * kWave
         : stream_blocks(silu, rows, cols, outs, E) * kStreamWaves * kWave;
     return threads < ((int64_t)1 << 32);
@@ -651,7 +675,7 @@ hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int row
                          const float* w_scales, int outs, bool silu, uint16_t* out,
                          hipStream_t stream)
 {
-    if (expert_large(rows, E)) {
+    if (expert_large(fp8, silu, rows, outs, E)) {
         const dim3 grid((unsigned)tile_blocks(silu, rows, outs, E));
         auto go = [&](auto kernel) {
             hipLaunchKernelGGL(kernel, grid, dim3(kTileWaves * kWave), 0, stream, (const uint8_t*)x,

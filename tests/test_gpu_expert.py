@@ -93,6 +93,8 @@ COUNTS = {
     "one_large": [1, 0, 300, 2],
     "last_only": [0] * 40 + [2],
     "many_experts": ([0, 1, 0, 2] * 256),
+    "ragged_large": [0, 130, 64, 65, 0, 1, 700, 2, 33, 0, 0, 15],
+    "many_larger": ([0, 11, 1, 24] * 256),
 }
 
 
@@ -101,7 +103,7 @@ COUNTS = {
 @pytest.mark.parametrize("counts", sorted(COUNTS))
 @pytest.mark.parametrize("cols,outs", [(128, 8), (384, 72), (1280, 200)])
 def test_products(counts, cols, outs, act, fp8):
-    if counts == "many_experts" and cols > 128:
+    if counts in ("many_experts", "many_larger") and cols > 128:
         pytest.skip("covered by the small size")
     print("expert %s C=%d D=%d %s fp8=%s" % (counts, cols, outs, act, fp8), flush=True)
     s = make(COUNTS[counts], cols, outs, act, fp8, seed=cols + outs)
