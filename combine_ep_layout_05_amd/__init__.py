@@ -343,17 +343,33 @@ def ep_topk_idx_narrow(topk_idx64, out_i32, stream=None):
 
 
 def _ptrs(stream, *tensors):
-    """The device pointers and the stream of one call, after checking that
-    everything lives on the current device (a kernel launched there could not
-    reach the others)."""
-    ptrs = [_ptr(t) for t in tensors]
-    dev = torch.cuda.current_device()
+    """The device pointers and the stream of one call, as integers, after
+    checking that everything lives on the current device (a kernel launched
+    there could not reach the others).  Kept short: at a few tokens the call,
+    not the kernel, is what a step waits for (torch.cuda.current_stream alone
+    takes 3 us, the launch 4)."""
+    ptrs, dev = [], -1
     for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, dev))
-    if stream is not None and stream.device.index != dev:
+        if t is None:
+            ptrs.append(None)
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError("device tensor expected, got a %s tensor" % t.device)
+        if not t.is_contiguous():
+            raise ValueError("contiguous tensor expected")
+        if dev >= 0 and d != dev:
+            raise ValueError("tensors on cuda:%d and cuda:%d in one call" % (dev, d))
+        dev = d
+        ptrs.append(t.data_ptr())
+    if dev != torch.cuda.current_device():
+        raise ValueError("tensors on cuda:%d, but the current device is cuda:%d" % (
+            dev, torch.cuda.current_device()))
+    if stream is None:
+        return ptrs, torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
         raise ValueError("stream on %s, but the current device is cuda:%d" % (stream.device, dev))
-    return ptrs, _stream(stream)
+    return ptrs, stream.cuda_stream
 
 
 def _choice(value, table, name):

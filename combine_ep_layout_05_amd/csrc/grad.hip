@@ -8,10 +8,15 @@
 // weight 1, is the reduce mode of combine.hip with K entries per token.)
 //
 // One workgroup per pair: its waves take 512-column steps in turn (16 bytes
-// per lane and load), each lane sums its products in fp32, and the waves'
-// sums are joined through LDS in wave order, so the result does not depend on
+// per lane and load), each lane sums its products in fp32, and the waves' sums
+// are joined through LDS in wave order, so the result does not depend on
 // timing.  The pairs of one token are neighbours on one XCD, so grad_out[t]
-// comes from HBM once and K - 1 times from that XCD's L2.
+// comes from HBM once and K - 1 times from that XCD's L2 (in launch order:
+// 6.8 -> 8.5 us at 128 x 7168 top-8, 191 -> 198 us at 4096 x 7168).
+//
+// It moves each byte once and runs at the rate of a copy: graphs of launches on
+// MI355X, 16384 x 4096 top-8 with 10 % of entries masked 411 us (5.0 TB/s; a 2
+// GiB copy 4.9), 4096 x 7168 191 us (5.2 TB/s), 128 x 7168 6.6 us.
 #include "ep_device.h"
 #include "ep_launch.h"
 #include "ep_numerics.h"
@@ -19,7 +24,6 @@
 namespace ep {
 namespace {
 
-constexpr int kGradWaves = 4;
 constexpr int kMaxGradBlocks = 1 << 20;
 
 __device__ __forceinline__ float wave_sum_f(float v)
@@ -29,6 +33,7 @@ __device__ __forceinline__ float wave_sum_f(float v)
     return v;
 }
 
+// o = bf16(w * g) and the sum of g * y over 8 columns.
 __device__ __forceinline__ float grad_step(uint4 g, uint4 y, float w, uint4& o)
 {
     const float gl[8] = {bf16_lo(g.x), bf16_hi(g.x), bf16_lo(g.y), bf16_hi(g.y),
@@ -45,44 +50,50 @@ __device__ __forceinline__ float grad_step(uint4 g, uint4 y, float w, uint4& o)
     return d;
 }
 
-template <bool kStream>
-__global__ __launch_bounds__(kGradWaves * kWave) void combine_backward_kernel(
+// kStream: rows touched once are loaded and stored nontemporally (4096 x 7168:
+// 205 us with cached stores, 202 with cached loads).
+template <bool kStream, int kWaves>
+__global__ __launch_bounds__(kWaves * kWave) void combine_backward_kernel(
     const uint16_t* __restrict__ grad_out, const uint16_t* __restrict__ y,
     const int32_t* __restrict__ row_of_pair, const float* __restrict__ topk_w, int n_pairs, int H,
     int K, uint16_t* __restrict__ grad_y, float* __restrict__ grad_w)
 {
-  __shared__ float part[kGradWaves];
-  for (int64_t first = 0; first < n_pairs; first += gridDim.x) {
-    const int in_grid = (int)min((int64_t)gridDim.x, n_pairs - first);
-    if ((int)blockIdx.x >= in_grid) return;
-    const int pair = (int)first + xcd_block(blockIdx.x, in_grid);
-    const int t = pair / K;
-    const int row = row_of_pair[pair];
-    const float w = topk_w[pair];
-    if (row < 0 || row >= n_pairs) {
-        if (threadIdx.x == 0) grad_w[pair] = 0.0f;
-        continue;
-    }
-    const uint16_t* const g = grad_out + (int64_t)t * H;
-    const uint16_t* const yr = y + (int64_t)row * H;
-    uint16_t* const o = grad_y + (int64_t)row * H;
-    float acc = 0.0f;
-    for (int c = threadIdx.x * kColsPerLane; c < H; c += kGradWaves * kStepCols) {
-        uint4 ov;
-        acc += grad_step(load16<false>(g + c), load16<kStream>(yr + c), w, ov);
-        store16<kStream>(o + c, ov);
-    }
-    acc = wave_sum_f(acc);
-    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = acc;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        float s = 0.0f;
+    __shared__ float part[kWaves];
+    for (int64_t first = 0; first < n_pairs; first += gridDim.x) {
+        const int in_grid = (int)min((int64_t)gridDim.x, n_pairs - first);
+        if ((int)blockIdx.x >= in_grid) return;
+        const int pair = (int)first + xcd_block(blockIdx.x, in_grid);
+        const int t = pair / K;
+        const int row = row_of_pair[pair];
+        const float w = topk_w[pair];
+        if (row < 0 || row >= n_pairs) {
+            if (threadIdx.x == 0) grad_w[pair] = 0.0f;
+            continue;
+        }
+        const uint16_t* const g = grad_out + (int64_t)t * H;
+        const uint16_t* const yr = y + (int64_t)row * H;
+        uint16_t* const o = grad_y + (int64_t)row * H;
+        float acc = 0.0f;
+        for (int64_t c = threadIdx.x * kColsPerLane; c < H; c += kWaves * kStepCols) {
+            uint4 ov;
+            acc += grad_step(load16<false>(g + c), load16<kStream>(yr + c), w, ov);
+            store16<kStream>(o + c, ov);
+        }
+        acc = wave_sum_f(acc);
+        if constexpr (kWaves == 1) {
+            if (threadIdx.x == 0) grad_w[pair] = acc;
+        } else {
+            if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = acc;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kGradWaves; ++i) s += part[i];
-        grad_w[pair] = s;
+                for (int i = 0; i < kWaves; ++i) s += part[i];
+                grad_w[pair] = s;
+            }
+            __syncthreads();                              // part is used again
+        }
     }
-    __syncthreads();                              // part is used again
-  }
 }
 
 }  // namespace
@@ -92,13 +103,20 @@ hipError_t launch_combine_backward(const uint16_t* grad_out, const uint16_t* y,
                                    int K, uint16_t* grad_y, float* grad_w, hipStream_t stream)
 {
     const int n = T * K;
-    const dim3 grid((unsigned)(n < kMaxGradBlocks ? n : kMaxGradBlocks)), block(kGradWaves * kWave);
-    if ((int64_t)n * H * 2 >= kStreamMinBytes)
-        hipLaunchKernelGGL(combine_backward_kernel<true>, grid, block, 0, stream, grad_out, y,
-                           row_of_pair, topk_w, n, H, K, grad_y, grad_w);
-    else
-        hipLaunchKernelGGL(combine_backward_kernel<false>, grid, block, 0, stream, grad_out, y,
-                           row_of_pair, topk_w, n, H, K, grad_y, grad_w);
+    const bool streaming = (int64_t)n * H * 2 >= kStreamMinBytes;
+    // Waves per pair.  Few pairs: 8 (2, 4, 8 waves: 4 x 6144 top-8 3.4, 2.8, 2.5
+    // us, 128 x 7168 7.2, 6.8, 6.6).  Many narrow ones: 1, as the waves of a
+    // pair would mostly wait for each other (1, 2, 4, 8 waves: 5000 x 1032 top-6
+    // 31.8, 35.9, 41.0, 65.4).  Otherwise 4; there the rate is the same within 2 %.
+    const int waves = n <= 2048 ? 8 : (H <= 3 * kStepCols ? 1 : 4);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(n < kMaxGradBlocks ? n : kMaxGradBlocks)),
+                           dim3(waves * kWave), 0, stream, grad_out, y, row_of_pair, topk_w, n, H,
+                           K, grad_y, grad_w);
+    };
+    if (waves == 8) streaming ? go(combine_backward_kernel<true, 8>) : go(combine_backward_kernel<false, 8>);
+    else if (waves == 4) streaming ? go(combine_backward_kernel<true, 4>) : go(combine_backward_kernel<false, 4>);
+    else streaming ? go(combine_backward_kernel<true, 1>) : go(combine_backward_kernel<false, 1>);
     return hipGetLastError();
 }
 

@@ -13,6 +13,8 @@ CASES = [  # T, H, E, K, share of masked entries
     (1, 8, 4, 1, 0.0), (1, 7168, 256, 8, 0.0), (4, 6144, 256, 8, 0.0), (3, 520, 16, 16, 0.3),
     (5, 1032, 8, 6, 0.5), (128, 7168, 288, 8, 0.0), (257, 2056, 64, 3, 0.1), (64, 1024, 2, 2, 0.9),
     (1021, 1032, 64, 6, 0.05), (2, 16392, 4, 2, 0.0),
+    # rows of 64 MiB and more (nontemporal accesses): wide, narrow, few; more pairs than workgroups
+    (2100, 2056, 64, 8, 0.1), (5500, 1032, 64, 6, 0.1), (512, 16392, 16, 4, 0.1), (70000, 8, 16, 16, 0.1),
 ]
 
 

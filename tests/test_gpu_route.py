@@ -47,7 +47,10 @@ def make(T, E, seed, dtype, spread=1.5):
 MODES = [("softmax", True, False), ("softmax", False, False), ("sigmoid", True, False),
          ("sigmoid", False, False), ("sigmoid", True, True), ("sigmoid", False, True)]
 SHAPES = [(1, 1, 1), (1, 8, 8), (3, 16, 16), (4, 256, 8), (5, 65, 2), (128, 288, 8), (7, 129, 6),
-          (33, 257, 4), (9, 511, 16), (130, 1024, 8), (2, 1000, 1), (1027, 100, 3)]
+          (33, 257, 4), (9, 511, 16), (130, 1024, 8), (2, 1000, 1), (1027, 100, 3),
+          # 16 lanes per token: aligned rows, rows of odd length, tokens left over in the last wave
+          (4096, 128, 8), (4099, 37, 16), (4097, 256, 2), (5003, 250, 6), (4098, 16, 1),
+          (8195, 128, 8), (8193, 61, 16)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -247,3 +250,19 @@ def test_route_graph_replays_and_streams():
         torch.cuda.synchronize()
         assert torch.equal(ids, eid) and torch.equal(w, ew) and torch.equal(gl, egl)
     graph.destroy()
+
+
+def test_more_tokens_than_the_grid_holds():
+    """2^24 + 5 tokens of two experts: the waves stride over the tokens."""
+    ep = ep_()
+    T = (1 << 24) + 5
+    l = torch.randn(T, 2, device="cuda")
+    ids, w = run(l, 1)
+    assert torch.equal(ids[:, 0].long(), (l[:, 1] > l[:, 0]).long())
+    assert bool((w == 1).all())
+    gl = torch.empty_like(l)
+    ep.ep_route_backward(l, ids, torch.ones_like(w), gl, renorm=False)
+    p = torch.softmax(l.double(), 1).gather(1, ids.long())
+    want = (p * (1 - p)).expand(T, 2) * torch.where(torch.arange(2, device="cuda")[None] == ids, 1.0, -1.0)
+    # the weights' relative error (a range below 16), once per factor
+    assert bool(((gl.double() - want).abs() <= 3 * (2 * 16 + 26) * EPS * 2 * p).all())
