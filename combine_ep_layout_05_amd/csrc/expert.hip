@@ -437,32 +437,35 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
     // buffer.
     const int so = (kSilu ? lane % kOuts + lane / kOuts * outs : lane) * blocks * 4;
     const int xso = min(wave * kTile + m, count - 1) * blocks * 4;
-    v4f wsv, xsv;
+    struct Scales { float w[kScaleBlocks], x[kScaleBlocks]; };
     auto load_scales = [&](int b) {
+        Scales v;
         if (blocks >= kScaleBlocks) {
             const int bl = min(b, blocks - kScaleBlocks);
-            wsv = __builtin_bit_cast(v4f, load_b128(sr, so, bl * 4));
-            if constexpr (kFp8) xsv = __builtin_bit_cast(v4f, load_b128(xsr, xso, bl * 4));
+            const v4f a = __builtin_bit_cast(v4f, load_b128(sr, so, bl * 4));
+            const v4f c = kFp8 ? __builtin_bit_cast(v4f, load_b128(xsr, xso, bl * 4)) : a;
+            v.w[0] = a[0]; v.w[1] = a[1]; v.w[2] = a[2]; v.w[3] = a[3];
+            v.x[0] = c[0]; v.x[1] = c[1]; v.x[2] = c[2]; v.x[3] = c[3];
         } else {
-            v4i a, c;
 #pragma unroll
             for (int i = 0; i < kScaleBlocks; ++i) {
-                a[i] = __builtin_amdgcn_raw_buffer_load_b32(sr, so, min(i, blocks - 1) * 4, 0);
-                c[i] = kFp8 ? __builtin_amdgcn_raw_buffer_load_b32(xsr, xso, min(i, blocks - 1) * 4, 0) : 0;
+                const int o = min(i, blocks - 1) * 4;
+                v.w[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sr, so, o, 0));
+                v.x[i] = kFp8 ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(xsr, xso, o, 0)) : 0.0f;
             }
-            wsv = __builtin_bit_cast(v4f, a);
-            xsv = __builtin_bit_cast(v4f, c);
         }
+        return v;
     };
-    auto store_scales = [&](int b, int buf) {
+    auto store_scales = [&](const Scales& v, int b, int buf) {
         const int skip = blocks >= kScaleBlocks ? b - min(b, blocks - kScaleBlocks) : 0;
 #pragma unroll
         for (int i = 0; i < kScaleBlocks; ++i) {
             if (i < skip) continue;
-            lds.ws[wave][i - skip][lane] = wsv[i];
-            if constexpr (kFp8) if (lane < kTile) lds.xs[buf][i - skip][wave * kTile + lane] = xsv[i];
+            lds.ws[wave][i - skip][lane] = v.w[i];
+            if constexpr (kFp8) if (lane < kTile) lds.xs[buf][i - skip][wave * kTile + lane] = v.x[i];
         }
     };
+
     // Block u of a stage, block i of the scales, kLive groups of 16 rows.
     auto compute = [&](auto kLive, auto& acc, const uint8_t* sx, int u, int buf, int i) {
         constexpr int kN = decltype(kLive)::value;
@@ -474,33 +477,34 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
         for (int j = 0; j < kColTiles; ++j)
             wc[j] = *(const v4i*)(lds.w[wave] + (j * kTile + m) * 128 + ((u * 4 + q) ^ (m % 8)) * 16);
         if constexpr (kFp8) {
-            // the products of a group are scaled and added while the next group's run
+            // every operand is asked for before the first product; the products
+            // of a group are scaled and added while the next group's run
             v4f sw[kColTiles], d[2][kColTiles];
-            float f[3];                          // of the group before, this one and the next
-            v8i xv[2];
+            float f[kN];
+            v8i xv[kN];
+#pragma unroll
+            for (int t = 0; t < kN; ++t) {
+                const v4i lo = x_at(t, u * 8 + q), hi = x_at(t, u * 8 + 4 + q);
+                xv[t] = (v8i){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            }
+#pragma unroll
+            for (int t = 0; t < kN; ++t) f[t] = lds.xs[buf][i][t * kTile + m];
 #pragma unroll
             for (int j = 0; j < kColTiles; ++j) sw[j] = *(const v4f*)&lds.ws[wave][i][j * kTile + q * 4];
-            auto get = [&](int t) {
-                const v4i lo = x_at(t, u * 8 + q), hi = x_at(t, u * 8 + 4 + q);
-                xv[t % 2] = (v8i){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                f[t % 3] = lds.xs[buf][i][t * kTile + m];
-            };
+            __builtin_amdgcn_sched_barrier(0);
             auto add = [&](int t, int j) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    acc[t][j][k] = __builtin_fmaf(d[t % 2][j][k], sw[j][k] * f[t % 3], acc[t][j][k]);
+                    acc[t][j][k] = __builtin_fmaf(d[t % 2][j][k], sw[j][k] * f[t], acc[t][j][k]);
             };
-            get(0);
 #pragma unroll
-            for (int t = 0; t < kN; ++t) {
-                if (t + 1 < kN) get(t + 1);
+            for (int t = 0; t < kN; ++t)
 #pragma unroll
                 for (int j = 0; j < kColTiles; ++j) {
-                    d[t % 2][j] = block_product(wc[j], xv[t % 2]);
+                    d[t % 2][j] = block_product(wc[j], xv[t]);
                     if (t > 0) add(t - 1, j);
                     __builtin_amdgcn_sched_barrier(0);
                 }
-            }
 #pragma unroll
             for (int j = 0; j < kColTiles; ++j) add(kN - 1, j);
         } else {
@@ -540,12 +544,12 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
         for (int t = 0; t < kN; ++t)
 #pragma unroll
             for (int j = 0; j < kColTiles; ++j) acc[t][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-        load_scales(0);
+        Scales scales = load_scales(0);
         load_x(0, 0);
         load_codes(0);
         for (int b0 = 0; b0 < blocks; b0 += kScaleBlocks) {
             const int buf = kFp8 ? (b0 / kScaleBlocks) % 2 : 0;
-            store_scales(b0, buf);
+            store_scales(scales, b0, buf);
 #pragma unroll
             for (int i = 0; i < kScaleBlocks; i += kStageBlocks) {
                 const int b = b0 + i;
@@ -553,7 +557,7 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
                 const bool more = b + kStageBlocks < blocks;
                 store_codes();
                 stage_barrier<0>();
-                if (i == 0 && b0 + kScaleBlocks < blocks) load_scales(b0 + kScaleBlocks);
+                if (i == 0 && b0 + kScaleBlocks < blocks) scales = load_scales(b0 + kScaleBlocks);
                 if constexpr (kFp8) {
                     const int cur = i / kStageBlocks;
                     if (more) { load_x(1 - cur, b + kStageBlocks); load_codes(b + kStageBlocks); }
@@ -561,7 +565,10 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
                     if (b + 1 < blocks) compute(kLive, acc, lds.x[cur], 1, buf, i + 1);
                 } else {
                     if (b + 1 < blocks) load_x(1, b + 1);
+                    asm volatile("" ::: "memory");       // in this order: the barrier below counts
+                    __builtin_amdgcn_sched_barrier(0);
                     if (more) load_codes(b + kStageBlocks);
+                    __builtin_amdgcn_sched_barrier(0);
                     compute(kLive, acc, lds.x[0], 0, buf, i);
                     if (b + 1 < blocks) {
                         // the rows of block b + 1; the codes after them may still be in flight
@@ -663,7 +670,7 @@ bool expert_launch_ok(bool fp8, bool silu, int rows, int cols, int outs, int E)
 {
     // offsets within a tile are 32-bit; a grid dimension holds fewer than 2^32 threads
     if (cols > kMaxExpertCols || outs > (1 << 29)) return false;
-    if (silu && (int64_t)outs * cols >= ((int64_t)1 << 36)) return false;
+    if (silu && (int64_t)outs * cols >= ((int64_t)1 << 35)) return false;
     const int64_t threads = expert_large(fp8, silu, rows, outs, E)
         ? tile_blocks(silu, rows, outs, E) * kTileWaves * kWave
         : stream_blocks(silu, rows, cols, outs, E) * kStreamWaves * kWave;

@@ -599,7 +599,7 @@ int ep_dispatch_backward(const uint16_t* grad_recv, const int32_t* row_of_pair, 
  * E outside 1..1024, cols or outs not positive or not divisible as above,
  * NULL or misaligned pointers (x, w, out 16 B, the rest 4 B) when rows > 0,
  * or sizes past the kernels' offsets and grids: cols > 2^23, outs > 2^29,
- * outs * cols >= 2^36 with EP_ACT_SILU_MUL, or a launch of 2^32 threads or
+ * outs * cols >= 2^35 with EP_ACT_SILU_MUL, or a launch of 2^32 threads or
  * more (from about rows * outs = 2^38 on).
  */
 #define EP_ACT_NONE 0

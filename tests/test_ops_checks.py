@@ -95,6 +95,8 @@ def test_expert_refusals():
     assert rc(_4=0) == -1 and rc(_4=1000) == -1 and rc(_9=0) == -1 and rc(_9=12) == -1
     assert rc(_6=0) == -1 and rc(_6=1025) == -1
     assert rc(_3=2**31 - 1) == -1                                    # grid limit
+    assert rc(_4=1 << 24) == -1 and rc(_9=1 << 30) == -1             # offset limits
+    assert rc(_4=1 << 20, _9=1 << 15) == -1
     for i in (0, 1, 5, 7, 8, 11):
         assert rc(**{"_%d" % i: NONE}) == -1 and rc(**{"_%d" % i: ODD}) == -1
     assert rc(_0=ctypes.c_void_p(0x10008)) == -1 and rc(_7=ctypes.c_void_p(0x10008)) == -1
