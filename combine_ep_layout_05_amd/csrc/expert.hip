@@ -4,11 +4,30 @@
 // Row r of expert e (expert_offset[e] <= r < expert_offset[e+1]):
 //   acc[r, n] = sum_b d[b] * s[e][n, b] * xs[r, b],
 //   d[b]      = sum over the 128 columns c of block b of x[r, c] * e2m1[e][n, c]
-// in fp32, blocks in ascending order (xs = 1 for bf16 rows).  One matrix
-// instruction per block and 16 x 16 outputs computes d when the rows are fp8:
-// it takes e4m3 and e2m1 operands as they are stored, and its 128 columns are
-// one scale block, so the scales are applied to its result.  bf16 rows take
-// four bf16 instructions per block on codes converted to bf16, which is exact.
+// in fp32 (xs = 1 for bf16 rows).  One matrix instruction per block and 16 x 16
+// outputs computes d when the rows are fp8: it takes e4m3 and e2m1 operands as
+// they are stored, and its 128 columns are one scale block, so the scales are
+// applied to its result.  bf16 rows take four bf16 instructions per block on
+// codes converted to bf16, which is exact.
+//
+// Rounding: the fp8 instruction adds the 16 products of a lane's 16 bytes in
+// fixed point, in steps of 2^-14 of the power of two below the largest one,
+// and everything after that in fp32 (read off the instruction; the bf16 one
+// keeps fp32 throughout).  An e4m3 value is itself rounded by up to 2^-4, 2^10
+// times as much; against 64 bits the outputs are off by 0.0017 (root mean
+// square, relative), as a product in 32 bits rounded once to bf16 is.  Sums
+// across blocks, scales and SiLU are fp32; the result is rounded to bf16 once.
+//
+// Two kernels share the batches: expert_stream_kernel for few rows per expert,
+// expert_tile_kernel for more (expert_large).  Both are bound by the bytes of
+// the weights up to about 30 rows per expert: 128 tokens, 288 experts, top-8 on
+// MI355X 675 us for gate and up (7168 columns, 2 x 2048 rows; 6.5 TB/s) and 375
+// us for down (2048 columns, 7168 rows; 5.9 TB/s); one token, 8 experts, 6144
+// columns, 2 x 2048 rows 21 us (5.1 TB/s).  At 128 rows per expert (4096 tokens,
+// Zipf routing) gate and up take 1.6 ms with fp8 rows (1.2 PFLOP/s, 2.7 TB/s)
+// and 2.3 ms with bf16 (0.83 PFLOP/s): there the matrix instructions and the
+// scaling of their results (8 vector instructions each) take half the time
+// each, and the two waves of a SIMD overlap them only in part.
 //
 // Operands: the weights are the A side (16 outputs n), the rows the B side
 // (16 rows m), so lane l holds the results of row m = l % 16 for the four
@@ -129,15 +148,17 @@ __device__ __forceinline__ v4i load_b128(__amdgpu_buffer_rsrc_t r, int lane_offs
 }
 
 // Few rows per expert: the weights are read once and bound the time, so the
-// work is split for loads in flight.  A workgroup of 8 waves takes 16 rows of
-// one expert and a share of the weight rows, 64 (silu: 32 + 32) at a time: a
-// group.  kSplit waves share a group, each with its own run of blocks; their
-// sums are joined through LDS in wave order (kSplit 1: nothing to join, and no
-// barrier).  A wave always has the codes and rows of its next block in flight,
-// across groups too.  The scales of its next 16 blocks are copied to a wave's
-// own part of LDS, transposed.
+// work is split for loads in flight.  A team of kSplit waves takes 16 rows of
+// one expert and 64 weight rows (silu: 32 + 32), each wave with its own run of
+// blocks; their sums are joined through LDS in wave order (kSplit 1: nothing to
+// join, and no barrier).  A wave takes two blocks at a time, whose codes are
+// whole cache lines (one at a time: 4.6 instead of 5.2 TB/s), and has the next
+// two in flight.  The scales of its next 16 blocks are copied to its own part
+// of LDS, transposed.  Nontemporal code loads drop a line between its two
+// halves here (5.5 -> 4.7 TB/s), and a team that goes on to further weight rows
+// gains nothing on more, shorter workgroups (4.9 -> 5.6 TB/s).
 constexpr int kStreamWaves = 4;
-constexpr int kStreamManyGroups = 4096, kStreamLongCols = 4096;
+constexpr int kStreamManyGroups = 2048, kStreamLongCols = 4096;
 constexpr int kGroupRows = 64;                    // weight rows per group: 4 operand tiles
 constexpr int kGroupTiles = kGroupRows / kTile;
 constexpr int kWindow = 16;                       // blocks whose scales are in LDS
@@ -309,6 +330,12 @@ __global__ __launch_bounds__(kStreamWaves * kWave, kFp8 ? 4 : 3) void expert_str
 //
 // The 16-byte pieces of a row in LDS are permuted (piece ^ row) so that 8
 // lanes reading one piece of 8 neighbouring rows meet 8 different banks.
+//
+// Also measured, 4096 tokens x 7168, gate and up, fp8: 128-row tiles in one
+// workgroup of 8 waves a CU 1.69 ms (nothing overlaps its prologue, and the
+// waves wait together); codes straight to registers in operand order 1.84 ms;
+// codes two stages ahead 1.67 ms; whole tiles of all experts before the rests
+// 1.80 ms (long and memory-bound tiles then no longer overlap).
 constexpr int kTileWaves = 4;
 constexpr int kTileRows = 64;                    // rows per workgroup
 constexpr int kRowTiles = kTileRows / kTile;
@@ -316,7 +343,9 @@ constexpr int kWaveCols = 64;                    // weight rows per wave: 4 oper
 constexpr int kColTiles = kWaveCols / kTile;
 constexpr int kStageBlocks = 2;
 constexpr int kCodeLoads = kWaveCols * kStageBlocks * 64 / 1024;                       // per wave
-constexpr int kChunkTiles = 4;                   // row tiles that run together on an XCD
+// Row tiles that run together on an XCD and share codes and rows in its L2 (1,
+// 2, 4, 8: 1.74, 1.66, 1.62, 1.74 ms at the size above).
+constexpr int kChunkTiles = 4;
 constexpr int kScaleBlocks = 4;                  // blocks per load of scales
 
 template <bool kFp8> struct TileShared {
@@ -377,7 +406,9 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
     if (!find_tile<kTileRows>(off, E, rows, tile, lane, expert, row0, count)) return;
     const int blocks = cols / kScaleBlock, half_cols = cols / 2;
     const int64_t wrows = (int64_t)outs * kParts;
-    // the expert's only tile: nobody else wants its codes in the L2
+    // the expert's only tile: nobody else wants its codes in the L2, and loaded
+    // nontemporally they come faster (512 tokens, 256 experts 434 -> 383 us; where
+    // tiles share them slower, 1.64 -> 1.81 ms at 4096 tokens)
     const bool alone = off[expert + 1] - off[expert] <= kTileRows;
 
     // (past the last output: other rows or 0, not stored)
@@ -621,18 +652,17 @@ int tile_groups(bool silu, int outs)
 }
 
 // Which kernel a batch runs, by its rows per expert (the routing is on the
-// device, so by their average).  Measured on MI355X, streaming against tiles,
-// gate and up products of 4096 columns:
-//   32 experts x 2 x 2048 weight rows (512 workgroups of tiles), fp8 rows: 40 /
-//   46 us at 1 row per expert, 52 / 47 at 2, 58 / 50 at 8, 116 / 55 at 32;
-//   bf16: 60 / 66 at 4, 69 / 67 at 8, 95 / 72 at 16;
-//   8 experts (128 workgroups, half the CUs), fp8: 17 / 37 at 8, 32 / 44 at 32,
-//   55 / 52 at 64; bf16: 42 / 65 at 32, 71 / 76 at 64.
-// (bf16 tiles take longer: the conversion of the codes is shared by few rows.)
-bool expert_large(bool fp8, bool silu, int rows, int outs, int E)
+// device, so by their average).  Measured on MI355X, streaming / tiles, gate
+// and up products of 4096 columns:
+//   32 experts x 2 x 2048 weight rows (512 workgroups of tiles), fp8 rows: 39 /
+//   45 us at 1 row per expert, 51 / 47 at 2, 57 / 49 at 8, 113 / 54 at 32; bf16:
+//   40 / 48, 53 / 49, 69 / 50, 149 / 66;
+//   8 experts (128 workgroups, half the CUs), fp8: 16 / 37 at 8, 32 / 45 at 32,
+//   54 / 53 at 64; bf16: 41 / 58 at 32, 69 / 70 at 64.
+bool expert_large(bool silu, int rows, int outs, int E)
 {
     const bool fill = (int64_t)E * tile_groups(silu, outs) >= 2 * kCUs;
-    return rows >= (fill ? (fp8 ? 2 : 8) : 64) * (int64_t)E;
+    return rows >= (fill ? 2 : 64) * (int64_t)E;
 }
 
 int64_t tile_blocks(bool silu, int rows, int outs, int E)
@@ -649,9 +679,11 @@ int stream_groups(bool silu, int outs)
 }
 
 // Waves that share a group in the streaming kernel: all four when the columns
-// are many or there are few groups, else one.  Measured (1 / 4 waves): 128
-// tokens, 288 experts, 2048 columns 406 / 470 us, 7168 columns 802 / 750 us; one
-// token, 8 experts x 6144 columns 32 / 21 us.
+// are many or there are few groups, else one.  Measured (1 / 4 waves): 288 rows
+// on 288 experts, 2048 columns x 7168 bf16 259 / 306 us, 4096 columns x 2 x 2048
+// fp8 292 / 277, 7168 columns 527 / 487; 32 rows on 32 experts, 2048 x 6144 (3264
+// groups) 45 / 48; 16 rows on 16 experts, 2048 x 2048 (544 groups) 15 / 10; one
+// token, 8 experts, 6144 columns 32 / 21.
 int stream_split(bool silu, int rows, int cols, int outs, int E)
 {
     const bool many = max_tiles(rows, E, kTile) * stream_groups(silu, outs) >= kStreamManyGroups;
@@ -666,12 +698,12 @@ int64_t stream_blocks(bool silu, int rows, int cols, int outs, int E)
 
 }  // namespace
 
-bool expert_launch_ok(bool fp8, bool silu, int rows, int cols, int outs, int E)
+bool expert_launch_ok(bool silu, int rows, int cols, int outs, int E)
 {
     // offsets within a tile are 32-bit; a grid dimension holds fewer than 2^32 threads
     if (cols > kMaxExpertCols || outs > (1 << 29)) return false;
     if (silu && (int64_t)outs * cols >= ((int64_t)1 << 35)) return false;
-    const int64_t threads = expert_large(fp8, silu, rows, outs, E)
+    const int64_t threads = expert_large(silu, rows, outs, E)
         ? tile_blocks(silu, rows, outs, E) * kTileWaves * kWave
         : stream_blocks(silu, rows, cols, outs, E) * kStreamWaves * kWave;
     return threads < ((int64_t)1 << 32);
@@ -682,7 +714,7 @@ hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int row
                          const float* w_scales, int outs, bool silu, uint16_t* out,
                          hipStream_t stream)
 {
-    if (expert_large(fp8, silu, rows, outs, E)) {
+    if (expert_large(silu, rows, outs, E)) {
         const dim3 grid((unsigned)tile_blocks(silu, rows, outs, E));
         auto go = [&](auto kernel) {
             hipLaunchKernelGGL(kernel, grid, dim3(kTileWaves * kWave), 0, stream, (const uint8_t*)x,
