@@ -12,6 +12,10 @@ raises.
     buf.layout(topk_idx_i32)                            # counts, offsets, slots
     buf.dispatch(x_bf16)                                # -> buf.recv_x, buf.recv_scales
     out = buf.combine(expert_out_bf16, topk_w_f32)      # -> bf16 [T, H]
+
+Beside the path: buf.route (logits -> topk_idx, topk_w), EpExpertsW4 (the
+experts' products with 4-bit weights on the receive rows), and the gradients
+(buf.combine_backward, buf.dispatch_backward, ep_route_backward).
 """
 from __future__ import annotations
 

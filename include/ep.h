@@ -20,6 +20,9 @@
  *     from the caller's buffer (MoRI PR #614 "perf(ep): InterNodeV1LL
  *     low-token latency on MI300X + CX7", zero-copy combine paragraph), and
  *     reduces them in fp32 with the top-k weights, written out as bf16.
+ * Beside the path: the router that makes the ids and weights (ep_route), the
+ * experts' products with 4-bit weights on the receive rows (ep_expert_w4) and
+ * the gradients of router, dispatch and combine (ep_*_backward).
  *
  * Conventions (all entry points):
  *   - Device pointers unless stated.  The caller owns every buffer; the
