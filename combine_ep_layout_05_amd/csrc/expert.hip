@@ -497,8 +497,69 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
         }
     };
 
-    // Block u of a stage, block i of the scales, kLive groups of 16 rows.
-    auto compute = [&](auto kLive, auto& acc, const uint8_t* sx, int u, int buf, int i) {
+    // fp8 rows: the kBlocks blocks of a stage, block i of the scales the first,
+    // kLive groups of 16 rows.  One sequence of (block, group) steps: each step's
+    // products start while those of the step before are scaled and added, and
+    // the operands of the second block are read while the first is computed
+    // (every wave reads at the start of a stage and none in between otherwise).
+    auto compute_fp8 = [&](auto kLive, auto kBlocks, auto& acc, const uint8_t* sx, int buf, int i) {
+        constexpr int kN = decltype(kLive)::value, kU = decltype(kBlocks)::value;
+        constexpr int kSlots = kN <= 2 ? 2 * kN : kN;        // few groups: both blocks' rows at once
+        v4i wc[kU][kColTiles];
+        v4f sw[kColTiles], d[kColTiles];         // of the block whose products are added
+        float f[kN];
+        v8i xv[kSlots];
+        auto get_w = [&](int u) {
+#pragma unroll
+            for (int j = 0; j < kColTiles; ++j)
+                wc[u][j] = *(const v4i*)(lds.w[wave] + (j * kTile + m) * 128 + ((u * 4 + q) ^ (m % 8)) * 16);
+        };
+        auto get_scales = [&](int u) {
+#pragma unroll
+            for (int t = 0; t < kN; ++t) f[t] = lds.xs[buf][i + u][t * kTile + m];
+#pragma unroll
+            for (int j = 0; j < kColTiles; ++j) sw[j] = *(const v4f*)&lds.ws[wave][i + u][j * kTile + q * 4];
+        };
+        auto get_x = [&](int u, int t) {
+            const uint8_t* const row = sx + (t * kTile + m) * S::kRowBytes;
+            const v4i lo = *(const v4i*)(row + ((u * 8 + q) ^ m) * 16);
+            const v4i hi = *(const v4i*)(row + ((u * 8 + 4 + q) ^ m) * 16);
+            xv[(u * kN + t) % kSlots] = (v8i){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        };
+        auto add = [&](int t, int j) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                acc[t][j][k] = __builtin_fmaf(d[j][k], sw[j][k] * f[t], acc[t][j][k]);
+        };
+        get_w(0);
+#pragma unroll
+        for (int t = 0; t < kN; ++t) get_x(0, t);
+        get_scales(0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int step = 0; step < kU * kN; ++step) {
+            const int u = step / kN, t = step % kN;
+#pragma unroll
+            for (int j = 0; j < kColTiles; ++j) {
+                if (step > 0) add((step - 1) % kN, j);
+                d[j] = block_product(wc[u][j], xv[step % kSlots]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (u + 1 < kU) {                                // the next block's operands
+                if (t == 0) get_w(u + 1);
+                if (kSlots == kN) get_x(u + 1, t);
+                else if (t == 0)
+#pragma unroll
+                    for (int r = 0; r < kN; ++r) get_x(u + 1, r);
+            }
+            if (u > 0 && t == 0) get_scales(u);              // (the block before is added by now)
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int j = 0; j < kColTiles; ++j) add(kN - 1, j);
+    };
+    // bf16 rows: block u of a stage, block i of the scales, kLive groups of 16 rows.
+    auto compute_bf16 = [&](auto kLive, auto& acc, const uint8_t* sx, int u, int buf, int i) {
         constexpr int kN = decltype(kLive)::value;
         auto x_at = [&](int t, int piece) {
             return *(const v4i*)(sx + (t * kTile + m) * S::kRowBytes + (piece ^ m) * 16);
@@ -507,63 +568,30 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
 #pragma unroll
         for (int j = 0; j < kColTiles; ++j)
             wc[j] = *(const v4i*)(lds.w[wave] + (j * kTile + m) * 128 + ((u * 4 + q) ^ (m % 8)) * 16);
-        if constexpr (kFp8) {
-            // every operand is asked for before the first product; the products
-            // of a group are scaled and added while the next group's run
-            v4f sw[kColTiles], d[2][kColTiles];
-            float f[kN];
-            v8i xv[kN];
+        v8bf xv[kN][4];
 #pragma unroll
-            for (int t = 0; t < kN; ++t) {
-                const v4i lo = x_at(t, u * 8 + q), hi = x_at(t, u * 8 + 4 + q);
-                xv[t] = (v8i){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            }
+        for (int t = 0; t < kN; ++t)
 #pragma unroll
-            for (int t = 0; t < kN; ++t) f[t] = lds.xs[buf][i][t * kTile + m];
+            for (int k = 0; k < 4; ++k) xv[t][k] = __builtin_bit_cast(v8bf, x_at(t, q * 4 + k));
 #pragma unroll
-            for (int j = 0; j < kColTiles; ++j) sw[j] = *(const v4f*)&lds.ws[wave][i][j * kTile + q * 4];
-            __builtin_amdgcn_sched_barrier(0);
-            auto add = [&](int t, int j) {
+        for (int j = 0; j < kColTiles; ++j) {
+            const v4f sw = *(const v4f*)&lds.ws[wave][i][j * kTile + q * 4];
+            v8bf wb[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    acc[t][j][k] = __builtin_fmaf(d[t % 2][j][k], sw[j][k] * f[t], acc[t][j][k]);
-            };
+            for (int k = 0; k < 4; ++k) wb[k] = bf16x8_of_codes((uint32_t)wc[j][k]);
+            v4f d[kN];
 #pragma unroll
-            for (int t = 0; t < kN; ++t)
+            for (int t = 0; t < kN; ++t) d[t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < kColTiles; ++j) {
-                    d[t % 2][j] = block_product(wc[j], xv[t]);
-                    if (t > 0) add(t - 1, j);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-#pragma unroll
-            for (int j = 0; j < kColTiles; ++j) add(kN - 1, j);
-        } else {
-            v8bf xv[kN][4];
-#pragma unroll
-            for (int t = 0; t < kN; ++t)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) xv[t][k] = __builtin_bit_cast(v8bf, x_at(t, q * 4 + k));
-#pragma unroll
-            for (int j = 0; j < kColTiles; ++j) {
-                const v4f sw = *(const v4f*)&lds.ws[wave][i][j * kTile + q * 4];
-                v8bf wb[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) wb[k] = bf16x8_of_codes((uint32_t)wc[j][k]);
-                v4f d[kN];
-#pragma unroll
-                for (int t = 0; t < kN; ++t) d[t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int t = 0; t < kN; ++t)
-                        d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[k], xv[t][k], d[t], 0, 0, 0);
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
                 for (int t = 0; t < kN; ++t)
+                    d[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[k], xv[t][k], d[t], 0, 0, 0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        acc[t][j][k] = __builtin_fmaf(d[t][k], sw[k], acc[t][j][k]);
-            }
+            for (int t = 0; t < kN; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    acc[t][j][k] = __builtin_fmaf(d[t][k], sw[k], acc[t][j][k]);
         }
     };
     // The whole product of kLive groups of 16 rows: a variant each, so that the
@@ -584,7 +612,7 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
 #pragma unroll
             for (int i = 0; i < kScaleBlocks; i += kStageBlocks) {
                 const int b = b0 + i;
-                if (b >= blocks) break;
+                if (b + (kFp8 ? 1 : 0) >= blocks) break;     // (fp8: a last single block follows the loop)
                 const bool more = b + kStageBlocks < blocks;
                 store_codes();
                 stage_barrier<0>();
@@ -592,23 +620,29 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
                 if constexpr (kFp8) {
                     const int cur = i / kStageBlocks;
                     if (more) { load_x(1 - cur, b + kStageBlocks); load_codes(b + kStageBlocks); }
-                    compute(kLive, acc, lds.x[cur], 0, buf, i);
-                    if (b + 1 < blocks) compute(kLive, acc, lds.x[cur], 1, buf, i + 1);
+                    compute_fp8(kLive, std::integral_constant<int, 2>(), acc, lds.x[cur], buf, i);
                 } else {
                     if (b + 1 < blocks) load_x(1, b + 1);
                     asm volatile("" ::: "memory");       // in this order: the barrier below counts
                     __builtin_amdgcn_sched_barrier(0);
                     if (more) load_codes(b + kStageBlocks);
                     __builtin_amdgcn_sched_barrier(0);
-                    compute(kLive, acc, lds.x[0], 0, buf, i);
+                    compute_bf16(kLive, acc, lds.x[0], 0, buf, i);
                     if (b + 1 < blocks) {
                         // the rows of block b + 1; the codes after them may still be in flight
                         if (more) stage_barrier<kCodeLoads>(); else stage_barrier<0>();
                         if (more) load_x(0, b + kStageBlocks);
-                        compute(kLive, acc, lds.x[1], 1, buf, i + 1);
+                        compute_bf16(kLive, acc, lds.x[1], 1, buf, i + 1);
                     }
                 }
             }
+        }
+        if (kFp8 && blocks % 2 != 0) {
+            const int b = blocks - 1;
+            store_codes();
+            stage_barrier<0>();
+            compute_fp8(kLive, std::integral_constant<int, 1>(), acc, lds.x[(b / kStageBlocks) % 2],
+                        (b / kScaleBlocks) % 2, b % kScaleBlocks);
         }
 #pragma unroll
         for (int t = 0; t < kN; ++t) {
