@@ -21,13 +21,13 @@
 // Two kernels share the batches: expert_stream_kernel for few rows per expert,
 // expert_tile_kernel for more (expert_large).  Both are bound by the bytes of
 // the weights up to about 30 rows per expert: 128 tokens, 288 experts, top-8 on
-// MI355X 675 us for gate and up (7168 columns, 2 x 2048 rows; 6.5 TB/s) and 375
-// us for down (2048 columns, 7168 rows; 5.9 TB/s); one token, 8 experts, 6144
+// MI355X 670 us for gate and up (7168 columns, 2 x 2048 rows; 6.5 TB/s) and 365
+// us for down (2048 columns, 7168 rows; 6.0 TB/s); one token, 8 experts, 6144
 // columns, 2 x 2048 rows 21 us (5.1 TB/s).  At 128 rows per expert (4096 tokens,
-// Zipf routing) gate and up take 1.6 ms with fp8 rows (1.2 PFLOP/s, 2.7 TB/s)
-// and 2.3 ms with bf16 (0.83 PFLOP/s): there the matrix instructions and the
-// scaling of their results (8 vector instructions each) take half the time
-// each, and the two waves of a SIMD overlap them only in part.
+// Zipf routing) gate and up take 1.55 ms with fp8 rows (1.24 PFLOP/s, 2.8 TB/s)
+// and 2.23 ms with bf16 (0.86 PFLOP/s).  There a matrix instruction and the 8
+// vector instructions that scale and add its result are the bound: 34 cycles
+// alone, 47 to 50 together with two waves a SIMD, however they are interleaved.
 //
 // Operands: the weights are the A side (16 outputs n), the rows the B side
 // (16 rows m), so lane l holds the results of row m = l % 16 for the four

@@ -101,7 +101,7 @@ COUNTS = {
 @pytest.mark.parametrize("act", ["none", "silu_mul"])
 @pytest.mark.parametrize("fp8", [True, False])
 @pytest.mark.parametrize("counts", sorted(COUNTS))
-@pytest.mark.parametrize("cols,outs", [(128, 8), (384, 72), (1280, 200)])
+@pytest.mark.parametrize("cols,outs", [(128, 8), (384, 72), (640, 40), (896, 264), (1152, 24), (1280, 200)])
 def test_products(counts, cols, outs, act, fp8):
     if counts in ("many_experts", "many_larger") and cols > 128:
         pytest.skip("covered by the small size")
