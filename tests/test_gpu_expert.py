@@ -230,10 +230,11 @@ def test_serving_step(T, H, I, E, K, payload):
     assert bool(((out.double() - terms.sum(1)).abs() <= bound * (1 + 2.0 ** -8)).all())
 
 
-def test_serving_step_captured():
+@pytest.mark.parametrize("T,E,K,payload", [(6, 16, 4, "fp8"), (200, 4, 2, "fp8"), (200, 4, 2, "bf16")])
+def test_serving_step_captured(T, E, K, payload):
     """The whole step in one graph, replayed on new tokens; and two of them on
     two streams at once, each with its own buffers."""
-    steps = [serving(6, 512, 256, 16, 4, "fp8", 3), serving(6, 512, 256, 16, 4, "fp8", 4)]
+    steps = [serving(T, 512, 256, E, K, payload, 3), serving(T, 512, 256, E, K, payload, 4)]
     graphs = []
     for ep, b, experts, x, logits in steps:
         s = torch.cuda.Stream()

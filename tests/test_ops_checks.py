@@ -232,3 +232,37 @@ def test_reference_gradients_match_differences():
                 lo, b, _ = opsref.route(l - d, K, score, None, renorm, 1.7)
                 assert np.array_equal(hi, ids) and np.array_equal(lo, ids)
                 np.testing.assert_allclose((up * (a - b)).sum(1) / (2 * h), grad[:, e], atol=1e-8)
+
+
+class FakeTensor:
+    """What the pointer check of a call looks at, on a made-up device."""
+
+    def __init__(self, device, contiguous=True):
+        self.index, self.contiguous, self.device = device, contiguous, "cuda:%d" % device
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def data_ptr(self):
+        return 4096
+
+
+def test_tensors_of_other_devices_are_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    here, there = FakeTensor(0), FakeTensor(1)
+    with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+        ep._ptrs(None, here, None, there)
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        ep._ptrs(None, there, there)
+    with pytest.raises(ValueError, match="contiguous"):
+        ep._ptrs(None, here, FakeTensor(0, contiguous=False))
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 77
+    with pytest.raises(ValueError, match="stream"):
+        ep._ptrs(Stream, here)
+    Stream.device = torch.device("cuda", 0)
+    assert ep._ptrs(Stream, here, None) == ([4096, None], 77)
