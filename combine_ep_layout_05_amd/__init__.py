@@ -514,7 +514,7 @@ def w4_quantise(weight):
     [..., C/2], scales fp32 [..., C/128]) as ep_expert_w4 takes them: per 128
     columns scale = amax / 6, codes the nearest e2m1 value of weight / scale,
     ties to the even code.  Plain torch, for laying weights out once."""
-    if weight.shape[-1] % SCALE_BLOCK:
+    if weight.dim() == 0 or weight.shape[-1] % SCALE_BLOCK:
         raise ValueError("weight: the last dimension must be a multiple of %d" % SCALE_BLOCK)
     blocks = weight.float().unflatten(-1, (-1, SCALE_BLOCK))
     scales = blocks.abs().amax(-1) / _E2M1[-1]
@@ -845,7 +845,10 @@ class EpExpertsW4:
 
     w_up uint8 [E, 2*I, H/2] (gate rows, then up rows), s_up fp32 [E, 2*I,
     H/128], w_down uint8 [E, H, I/2], s_down fp32 [E, H, I/128]: codes and
-    scales as w4_quantise lays them out; I % 128 == 0."""
+    scales as w4_quantise lays them out; I % 128 == 0.
+
+    One call at a time: calls, and replays of graphs that hold them, on two
+    streams need an object each (which may share the weights), as EpBuffers do."""
 
     def __init__(self, T, K, w_up, s_up, w_down, s_down):
         for w, sc in ((w_up, s_up), (w_down, s_down)):

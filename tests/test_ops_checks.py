@@ -266,3 +266,9 @@ def test_tensors_of_other_devices_are_refused(monkeypatch):
         ep._ptrs(Stream, here)
     Stream.device = torch.device("cuda", 0)
     assert ep._ptrs(Stream, here, None) == ([4096, None], 77)
+
+
+@pytest.mark.parametrize("shape", [(), (127,), (4, 129)])
+def test_quantise_refuses_partial_blocks(shape):
+    with pytest.raises(ValueError, match="multiple of 128"):
+        ep.w4_quantise(torch.zeros(shape))
