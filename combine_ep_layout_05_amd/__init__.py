@@ -376,6 +376,24 @@ def _ptrs(stream, *tensors):
     return ptrs, stream.cuda_stream
 
 
+def _new(stream, make):
+    """An output that a call on `stream` writes, when the caller gave none.  It
+    is made on that stream: filled anywhere else, the fill could land after the
+    call's kernel, and its memory could still be in use.  The current stream is
+    recorded as its second user, so that it can be dropped while work queued
+    there still reads it."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        if stream != here and torch.cuda.is_current_stream_capturing():
+            raise ValueError("outputs must be given when the call is captured into a graph: "
+                             "memory made here could be freed while the graph lives")
+        t = make()
+    t.record_stream(here)
+    return t
+
+
 def _choice(value, table, name):
     v = table.get(value, value)
     if v not in table.values() or isinstance(v, bool):
@@ -812,23 +830,26 @@ class EpBuffers:
                          grad_topk_w=None, stream=None):
         """The combine's gradient for the current batch: grad_out bf16 [n, H] ->
         (grad_expert_out bf16 [n*K, H], grad_topk_w fp32 [n, K]).  Outputs not
-        given are allocated, grad_expert_out as zeros (rows without a pair are
-        not written); give them when the call is captured into a graph."""
+        given are allocated on the call's stream, grad_expert_out as zeros (rows
+        without a pair are not written); give them when the call is captured
+        into a graph."""
         _same_tokens(self, topk_w.shape[0], "topk_w")
         _same_tokens(self, grad_out.shape[0], "grad_out")
         if grad_expert_out is None:
-            grad_expert_out = torch.zeros_like(expert_out[:self.n * self.K])
+            grad_expert_out = _new(stream, lambda: torch.zeros_like(expert_out[:self.n * self.K]))
         if grad_topk_w is None:
-            grad_topk_w = torch.empty_like(topk_w)
+            grad_topk_w = _new(stream, lambda: torch.empty_like(topk_w))
         ep_combine_backward(grad_out, expert_out, self._views(self.n)[0], topk_w, grad_expert_out,
                             grad_topk_w, stream)
         return grad_expert_out, grad_topk_w
 
     def dispatch_backward(self, grad_recv, grad_x=None, stream=None):
         """The dispatch's gradient for the current batch: grad_recv bf16
-        [>= n*K, H] -> grad_x bf16 [n, H] (allocated when not given)."""
+        [>= n*K, H] -> grad_x bf16 [n, H] (allocated on the call's stream when
+        not given; give it when the call is captured into a graph)."""
         if grad_x is None:
-            grad_x = torch.empty((self.n, self.H), dtype=torch.bfloat16, device=grad_recv.device)
+            grad_x = _new(stream, lambda: torch.empty((self.n, self.H), dtype=torch.bfloat16,
+                                                      device=grad_recv.device))
         _same_tokens(self, grad_x.shape[0], "grad_x")
         ep_dispatch_backward(grad_recv, self._views(self.n)[0], grad_x, stream)
         return grad_x

@@ -239,3 +239,27 @@ def test_batch_below_the_capacity():
     assert torch.equal(gy[row], want)
     with pytest.raises(ValueError, match="tokens"):
         b.combine_backward(go[:10], y, w)
+
+
+def test_missing_outputs_on_a_stream_beside_a_busy_one():
+    """Outputs that the call allocates are filled on its own stream: work that
+    is still queued on the current stream neither delays the fill until after
+    the kernel nor uses the same memory."""
+    ep, b, go, y, w = setup(64, 2048, 32, 8, 0.2, seed=12)
+    ey, ew = b.combine_backward(go, y, w)
+    ex = b.dispatch_backward(ey)
+    a = torch.randn(8192, 8192, device="cuda", dtype=torch.bfloat16)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for _ in range(20):
+            a @ a                                     # tens of milliseconds on the current stream
+        gone = torch.full_like(y, 5.0)                # and memory it still writes when freed
+        del gone
+        gy, gw = b.combine_backward(go, y, w, stream=s)
+        gx = b.dispatch_backward(gy, stream=s)
+        s.synchronize()
+        got = [t.clone() for t in (gy, gw, gx)]       # on the current stream, after all of its work
+        torch.cuda.synchronize()
+        for t, e in zip(got, (ey, ew, ex)):
+            assert torch.equal(t, e)

@@ -272,3 +272,68 @@ def test_tensors_of_other_devices_are_refused(monkeypatch):
 def test_quantise_refuses_partial_blocks(shape):
     with pytest.raises(ValueError, match="multiple of 128"):
         ep.w4_quantise(torch.zeros(shape))
+
+
+class FakeStream:
+    device, cuda_stream = torch.device("cuda", 0), 99
+
+
+@pytest.fixture
+def fake_streams(monkeypatch):
+    """A current stream `here` and torch.cuda.stream as a record of which one
+    is current; `made` lists (maker, stream it ran under)."""
+    here, made, now = FakeStream(), [], []
+    now.append(here)
+
+    class Use:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            now.append(self.s)
+
+        def __exit__(self, *exc):
+            now.pop()
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now[-1])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, s: made.append(("record", s)))
+    for name in ("zeros_like", "empty_like", "empty", "zeros"):
+        def maker(*a, _f=getattr(torch, name), _n=name, **kw):
+            made.append((_n, now[-1]))
+            return _f(*a, **kw)
+        monkeypatch.setattr(torch, name, maker)
+    for name in ("ep_combine_backward", "ep_dispatch_backward"):
+        monkeypatch.setattr(ep, name, lambda *a, _n=name: made.append((_n, a[-1])))
+    return here, made
+
+
+def test_missing_outputs_are_made_on_the_calls_stream(fake_streams, monkeypatch):
+    """The fill of an output and its memory belong to the stream that the
+    kernel runs on: on another they are not ordered with it."""
+    here, made = fake_streams
+    b = ep.EpBuffers(4, 384, 2, 3, 1, device="cpu")
+    go, y, w = torch.ones(4, 384), torch.ones(8, 384), torch.ones(4, 2)
+    s = FakeStream()
+    del made[:]
+    b.combine_backward(go, y, w, stream=s)
+    b.dispatch_backward(y, stream=s)
+    assert [m for m in made if m[0] != "record"] == [
+        ("zeros_like", s), ("empty_like", s), ("ep_combine_backward", s),
+        ("empty", s), ("ep_dispatch_backward", s)]
+    assert [m for m in made if m[0] == "record"] == [("record", here)] * 3
+    del made[:]
+    b.combine_backward(go, y, w)
+    b.dispatch_backward(y)
+    assert [m[1] for m in made if not m[0].startswith("ep_")] == [here] * 3
+    # captured on a stream that torch's allocator knows nothing of: refused, not made
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    del made[:]
+    for call in (lambda: b.combine_backward(go, y, w, stream=s),
+                 lambda: b.combine_backward(go, y, w, torch.ones_like(y), stream=s),
+                 lambda: b.dispatch_backward(y, stream=s)):
+        with pytest.raises(ValueError, match="outputs must be given"):
+            call()
+    assert not [m for m in made if m[0].startswith("ep_") or m[0] in ("empty", "zeros_like", "empty_like")
+                and m[1] is s]
