@@ -667,7 +667,7 @@ int ep_expert_w4(const void* x, const float* x_scales, int payload, int rows, in
     if (rows < 0 || E < 1 || E > EP_MAX_EXPERTS || cols <= 0 || cols % ep::kScaleBlock != 0 ||
         outs <= 0 || outs % 8 != 0)
         return EP_EINVAL;
-    if (!ep::expert_launch_ok(act == EP_ACT_SILU_MUL, rows, cols, outs, E))
+    if (!ep::expert_launch_ok(payload == EP_PAYLOAD_FP8_E4M3FN, act == EP_ACT_SILU_MUL, rows, cols, outs, E))
         return EP_EINVAL;
     if (rows == 0) return EP_OK;
     if (!ptr_ok(x, 16) || !ptr_ok(expert_offset, 4) || !ptr_ok(w, 16) || !ptr_ok(w_scales, 4) ||

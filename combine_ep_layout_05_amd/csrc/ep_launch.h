@@ -114,7 +114,7 @@ hipError_t launch_combine_backward(const uint16_t* grad_out, const uint16_t* y,
 
 // Whether launch_expert takes a batch of `rows` receive rows of `cols` columns
 // and `outs` outputs.
-bool expert_launch_ok(bool silu, int rows, int cols, int outs, int E);
+bool expert_launch_ok(bool fp8, bool silu, int rows, int cols, int outs, int E);
 
 hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int rows, int cols,
                          const int32_t* expert_offset, int E, const uint8_t* w,

@@ -4,30 +4,39 @@
 // Row r of expert e (expert_offset[e] <= r < expert_offset[e+1]):
 //   acc[r, n] = sum_b d[b] * s[e][n, b] * xs[r, b],
 //   d[b]      = sum over the 128 columns c of block b of x[r, c] * e2m1[e][n, c]
-// in fp32 (xs = 1 for bf16 rows).  One matrix instruction per block and 16 x 16
-// outputs computes d when the rows are fp8: it takes e4m3 and e2m1 operands as
-// they are stored, and its 128 columns are one scale block, so the scales are
-// applied to its result.  bf16 rows take four bf16 instructions per block on
+// in fp32 (xs = 1 for bf16 rows).  Two matrix instructions per block and 16 x 16
+// outputs compute d when the rows are fp8: they take e4m3 and e2m1 operands as
+// they are stored, and their 128 columns are one scale block, so the scales are
+// applied to the result.  bf16 rows take four bf16 instructions per block on
 // codes converted to bf16, which is exact.
 //
 // Rounding: the fp8 instruction adds the 16 products of a lane's 16 bytes in
-// fixed point, in steps of 2^-14 of the power of two below the largest one,
-// and everything after that in fp32 (read off the instruction; the bf16 one
-// keeps fp32 throughout).  An e4m3 value is itself rounded by up to 2^-4, 2^10
-// times as much; against 64 bits the outputs are off by 0.0017 (root mean
-// square, relative), as a product in 32 bits rounded once to bf16 is.  Sums
-// across blocks, scales and SiLU are fp32; the result is rounded to bf16 once.
+// fixed point, in steps of 2^-14 of the power of two below the largest one, and
+// drops what lies below (read off the instruction; everything after that it
+// adds in fp32, and the bf16 one keeps fp32 throughout).  Next to a row's 448,
+// products below 1/8 would be lost, and sums in which large products cancel
+// would be wrong by many times their value.  So the values below 2 and those
+// from 2 on go through it apart.  e2m1 values are multiples of 2^-1 up to 6, and
+// e4m3 values below 2 multiples of 2^-9: their products are multiples of 2^-10
+// below 2^3.5, at most 2^13 steps; values from 2 on are multiples of 2^-2 up to
+// 448, the products multiples of 2^-3 below 2^11.4, at most 2^14.4 steps of
+// which the lowest is 2^-14 of 2^11.  Both sums of 16 are exact, and all the
+// others are fp32.  One instruction on the whole values takes 1.59 ms where the
+// two take 2.17 (4096 tokens x 7168, gate and up, see below); where the weights'
+// bytes are the bound they cost nothing.  Sums across blocks, scales and SiLU
+// are fp32; the result is rounded to bf16 once.
 //
 // Two kernels share the batches: expert_stream_kernel for few rows per expert,
 // expert_tile_kernel for more (expert_large).  Both are bound by the bytes of
 // the weights up to about 30 rows per expert: 128 tokens, 288 experts, top-8 on
-// MI355X 670 us for gate and up (7168 columns, 2 x 2048 rows; 6.5 TB/s) and 365
+// MI355X 695 us for gate and up (7168 columns, 2 x 2048 rows; 6.3 TB/s) and 365
 // us for down (2048 columns, 7168 rows; 6.0 TB/s); one token, 8 experts, 6144
-// columns, 2 x 2048 rows 21 us (5.1 TB/s).  At 128 rows per expert (4096 tokens,
-// Zipf routing) gate and up take 1.55 ms with fp8 rows (1.24 PFLOP/s, 2.8 TB/s)
-// and 2.23 ms with bf16 (0.86 PFLOP/s).  There a matrix instruction and the 8
-// vector instructions that scale and add its result are the bound: 34 cycles
-// alone, 47 to 50 together with two waves a SIMD, however they are interleaved.
+// columns, 2 x 2048 rows 21.5 us (5.0 TB/s).  At 128 rows per expert (4096 tokens,
+// Zipf routing) gate and up take 2.17 ms with fp8 rows (0.89 PFLOP/s) and 2.23
+// ms with bf16 (0.86 PFLOP/s): twice 32 and four times 16 cycles of the matrix
+// unit per 16 x 16 outputs and block (1.5 ms in all at the rate a library product
+// reaches), beside 8 vector instructions that scale and add the result and, fp8,
+// 8 that part the rows.
 //
 // Operands: the weights are the A side (16 outputs n), the rows the B side
 // (16 rows m), so lane l holds the results of row m = l % 16 for the four
@@ -112,15 +121,39 @@ __device__ __forceinline__ v8bf bf16x8_of_codes(uint32_t codes)
     return __builtin_bit_cast(v8bf, v);
 }
 
-// d of one block for 16 outputs x 16 rows.
-__device__ __forceinline__ v4f block_product(v4i w, v8i x)
+// Four e4m3 values of a row in two parts whose sum they are: those below 2
+// (returned in x) and those from 2 on, NaN among them, which are the bytes with
+// bit 6 set; the other part's byte is 0.  One selector (byte i of x where it is
+// from 2 on, else of 0) serves both.
+__device__ __forceinline__ uint32_t take_high(uint32_t& x)
 {
-    const v8i a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
-    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    // cbsz 4: A is e2m1; blgp 0: B is e4m3; no block scales (the unscaled form)
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, x, zero, 4, 0, 0, 0, 0, 0);
+    const uint32_t sel = ((x >> 4) & 0x04040404u) | 0x03020100u;
+    const uint32_t high = __builtin_amdgcn_perm(x, 0u, sel);
+    x = __builtin_amdgcn_perm(0u, x, sel);
+    return high;
 }
 
+__device__ __forceinline__ v8i take_high(v8i& x)
+{
+    v8i high;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t v = (uint32_t)x[i];
+        high[i] = (int)take_high(v);
+        x[i] = (int)v;
+    }
+    return high;
+}
+
+// c + the products of one block for 16 outputs x 16 rows, of one part of the rows.
+__device__ __forceinline__ v4f part_product(v4i w, v8i x, v4f c)
+{
+    const v8i a = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+    // cbsz 4: A is e2m1; blgp 0: B is e4m3; no block scales (the unscaled form)
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, x, c, 4, 0, 0, 0, 0, 0);
+}
+
+// d of one block for 16 outputs x 16 rows, bf16.
 __device__ __forceinline__ v4f block_product(v4i w, const v4i (&x)[4])
 {
     v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -148,7 +181,7 @@ __device__ __forceinline__ v4i load_b128(__amdgpu_buffer_rsrc_t r, int lane_offs
 }
 
 // Few rows per expert: the weights are read once and bound the time, so the
-// work is split for loads in flight.  A team of kSplit waves takes 16 rows of
+// work is split for loads in flight.  A team of kSplit waves takes kRows rows of
 // one expert and 64 weight rows (silu: 32 + 32), each wave with its own run of
 // blocks; their sums are joined through LDS in wave order (kSplit 1: nothing to
 // join, and no barrier).  A wave takes two blocks at a time, whose codes are
@@ -164,8 +197,12 @@ constexpr int kGroupTiles = kGroupRows / kTile;
 constexpr int kWindow = 16;                       // blocks whose scales are in LDS
 constexpr int kScalePitch = kGroupRows + kTile + 4;   // weight rows, then fp8 rows
 
-template <bool kFp8, bool kSilu, int kSplit>
-__global__ __launch_bounds__(kStreamWaves * kWave, kFp8 ? 4 : 3) void expert_stream_kernel(
+//
+// kRows 8, fp8 rows: the two parts of a row are two of the 16 rows of one matrix
+// instruction (lanes m and m + 8), whose sums are joined at the end.  kRows 16:
+// two instructions.
+template <bool kFp8, bool kSilu, int kSplit, int kRows>
+__global__ __launch_bounds__(kStreamWaves * kWave, kRows < kTile ? 4 : 3) void expert_stream_kernel(
     const uint8_t* __restrict__ x, const float* __restrict__ xs, int rows, int cols,
     const int32_t* __restrict__ off, int E, const uint8_t* __restrict__ w,
     const float* __restrict__ ws, int outs, uint16_t* __restrict__ out, int n_groups,
@@ -174,12 +211,14 @@ __global__ __launch_bounds__(kStreamWaves * kWave, kFp8 ? 4 : 3) void expert_str
     constexpr int kTeams = kStreamWaves / kSplit;                   // groups at a time
     constexpr int kOuts = kSilu ? kGroupRows / 2 : kGroupRows;      // outputs per group
     constexpr int kHalf = kOuts / kTile;                            // operand tiles of results
+    constexpr bool kPaired = kRows < kTile;
+    static_assert(kRows == kTile || (kFp8 && kRows == kTile / 2), "a row, or the two parts of an fp8 row, per lane");
     __shared__ __attribute__((aligned(16))) float s_scale[kStreamWaves][kWindow * kScalePitch];
     __shared__ v4f s_part[kSplit > 1 ? kStreamWaves : 1][kGroupTiles][kWave];
     const int lane = threadIdx.x % kWave, m = lane % kTile, q = lane / kTile;
     const int wave = wave_uniform(threadIdx.x / kWave), team = wave / kSplit, part = wave % kSplit;
     int expert, row0, count;
-    if (!find_tile<kTile>(off, E, rows, blockIdx.x / n_parts, lane, expert, row0, count)) return;
+    if (!find_tile<kRows>(off, E, rows, blockIdx.x / n_parts, lane, expert, row0, count)) return;
     const int blocks = cols / kScaleBlock;
     const int run = ((blocks + 1) / 2 + kSplit - 1) / kSplit * 2;   // blocks per wave, in pairs
     const int b0 = min(part * run, blocks), b1 = min(b0 + run, blocks);
@@ -191,7 +230,7 @@ __global__ __launch_bounds__(kStreamWaves * kWave, kFp8 ? 4 : 3) void expert_str
     constexpr int kRowBytes = kFp8 ? 1 : 2;
     const __amdgpu_buffer_rsrc_t xr = buffer(x + (int64_t)row0 * cols * kRowBytes, (int64_t)count * cols * kRowBytes);
     const __amdgpu_buffer_rsrc_t xsr = buffer(kFp8 ? xs + (int64_t)row0 * blocks : nullptr, kFp8 ? (int64_t)count * blocks * 4 : 0);
-    const int xo = min(m, count - 1) * cols * kRowBytes + q * (kFp8 ? 16 : 64);
+    const int xo = min(m % kRows, count - 1) * cols * kRowBytes + q * (kFp8 ? 16 : 64);
     const int wo = m * half_cols + q * 16;
 
     // first weight row of part h of group g
@@ -268,15 +307,21 @@ __global__ __launch_bounds__(kStreamWaves * kWave, kFp8 ? 4 : 3) void expert_str
             for (int u = 0; u < 2; ++u) {
                 if (b + u >= b1) break;
                 const float* const sb = sc + (at + u) * kScalePitch;
-                const float f = kFp8 ? sb[kGroupRows + m] : 1.0f;
+                const float f = kFp8 ? sb[kGroupRows + m % kRows] : 1.0f;
+                v8i high{}, low{};
+                if constexpr (kFp8) {
+                    low = (v8i){xv[u][0][0], xv[u][0][1], xv[u][0][2], xv[u][0][3],
+                                xv[u][1][0], xv[u][1][1], xv[u][1][2], xv[u][1][3]};
+                    high = take_high(low);
+                    if (kPaired && m >= kRows) high = low;
+                }
 #pragma unroll
                 for (int j = 0; j < kGroupTiles; ++j) {
                     const v4f sw = *(const v4f*)(sb + j * kTile + q * 4);
                     v4f d;
                     if constexpr (kFp8) {
-                        const v8i x8 = {xv[u][0][0], xv[u][0][1], xv[u][0][2], xv[u][0][3],
-                                        xv[u][1][0], xv[u][1][1], xv[u][1][2], xv[u][1][3]};
-                        d = block_product(cur.w[u][j], x8);
+                        d = part_product(cur.w[u][j], high, (v4f){0.0f, 0.0f, 0.0f, 0.0f});
+                        if (!kPaired) d = part_product(cur.w[u][j], low, d);
                     } else {
                         d = block_product(cur.w[u][j], xv[u]);
                     }
@@ -286,6 +331,16 @@ __global__ __launch_bounds__(kStreamWaves * kWave, kFp8 ? 4 : 3) void expert_str
             }
             cur = next;
         }
+    }
+    if constexpr (kPaired) {                          // the low parts' sums are 8 lanes on
+#pragma unroll
+        for (int j = 0; j < kGroupTiles; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float mine = acc[j][i];
+                acc[j][i] = mine + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                    0, __builtin_bit_cast(int, mine), 0x128, 0xF, 0xF, false));        // row_ror 8
+            }
     }
     // operand tile j of lane ln: row ln % 16, outputs (ln / 16) * 4 .. + 3 of the tile
     auto store = [&](int j, int ln, v4f v, v4f u) {
@@ -498,10 +553,12 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
     };
 
     // fp8 rows: the kBlocks blocks of a stage, block i of the scales the first,
-    // kLive groups of 16 rows.  One sequence of (block, group) steps: each step's
-    // products start while those of the step before are scaled and added, and
-    // the operands of the second block are read while the first is computed
-    // (every wave reads at the start of a stage and none in between otherwise).
+    // kLive groups of 16 rows.  One sequence of (block, group) steps: the products
+    // of a step's low values start while those of the step before are scaled and
+    // added, those of its high values while the next step's rows are parted (in
+    // another order, or left to the compiler, 1-2 % slower), and the operands of
+    // the second block are read while the first is computed (every wave reads at
+    // the start of a stage and none in between otherwise).
     auto compute_fp8 = [&](auto kLive, auto kBlocks, auto& acc, const uint8_t* sx, int buf, int i) {
         constexpr int kN = decltype(kLive)::value, kU = decltype(kBlocks)::value;
         constexpr int kSlots = kN <= 2 ? 2 * kN : kN;        // few groups: both blocks' rows at once
@@ -535,14 +592,30 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
 #pragma unroll
         for (int t = 0; t < kN; ++t) get_x(0, t);
         get_scales(0);
+        v8i high = take_high(xv[0]);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int step = 0; step < kU * kN; ++step) {
             const int u = step / kN, t = step % kN;
+            v8i& low = xv[step % kSlots];
+            v8i& next = xv[(step + 1) % kSlots];
 #pragma unroll
             for (int j = 0; j < kColTiles; ++j) {
                 if (step > 0) add((step - 1) % kN, j);
-                d[j] = block_product(wc[u][j], xv[step % kSlots]);
+                d[j] = part_product(wc[u][j], low, (v4f){0.0f, 0.0f, 0.0f, 0.0f});
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            v8i next_high{};
+#pragma unroll
+            for (int j = 0; j < kColTiles; ++j) {
+                if (kN > 1 && step + 1 < kU * kN)
+#pragma unroll
+                    for (int i = 2 * j; i < 2 * j + 2; ++i) {
+                        uint32_t v = (uint32_t)next[i];
+                        next_high[i] = (int)take_high(v);
+                        next[i] = (int)v;
+                    }
+                d[j] = part_product(wc[u][j], high, d[j]);
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (u + 1 < kU) {                                // the next block's operands
@@ -553,6 +626,8 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
                     for (int r = 0; r < kN; ++r) get_x(u + 1, r);
             }
             if (u > 0 && t == 0) get_scales(u);              // (the block before is added by now)
+            if (kN == 1 && step + 1 < kU) next_high = take_high(next);
+            high = next_high;
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -712,34 +787,42 @@ int stream_groups(bool silu, int outs)
     return (int)(((int64_t)outs + per - 1) / per);
 }
 
+// Rows per team of the streaming kernel: 16, or 8 where fp8 rows are few and the
+// two parts of all of them fit one matrix instruction, which leaves registers
+// for a fourth wave per SIMD.  4096 columns x 2 x 2048, 8 / 16: 29.3 / 32.4 us
+// with 24 experts of 1 row, 29.0 / 31.5 with 16 of 2, 277 / 281 with 288 of 1,
+// otherwise the same up to 2 rows; with 8 experts 19.7 / 16.3 at 4 rows, 23.5 /
+// 16.6 at 8, 56 / 33 at 32 (each team reads the codes again).
+int stream_rows(bool fp8, int rows, int E) { return fp8 && rows < 3 * (int64_t)E ? kTile / 2 : kTile; }
+
 // Waves that share a group in the streaming kernel: all four when the columns
 // are many or there are few groups, else one.  Measured (1 / 4 waves): 288 rows
 // on 288 experts, 2048 columns x 7168 bf16 259 / 306 us, 4096 columns x 2 x 2048
 // fp8 292 / 277, 7168 columns 527 / 487; 32 rows on 32 experts, 2048 x 6144 (3264
 // groups) 45 / 48; 16 rows on 16 experts, 2048 x 2048 (544 groups) 15 / 10; one
 // token, 8 experts, 6144 columns 32 / 21.
-int stream_split(bool silu, int rows, int cols, int outs, int E)
+int stream_split(bool fp8, bool silu, int rows, int cols, int outs, int E)
 {
-    const bool many = max_tiles(rows, E, kTile) * stream_groups(silu, outs) >= kStreamManyGroups;
+    const bool many = max_tiles(rows, E, stream_rows(fp8, rows, E)) * stream_groups(silu, outs) >= kStreamManyGroups;
     return many && cols < kStreamLongCols ? 1 : kStreamWaves;
 }
 
-int64_t stream_blocks(bool silu, int rows, int cols, int outs, int E)
+int64_t stream_blocks(bool fp8, bool silu, int rows, int cols, int outs, int E)
 {
-    const int teams = kStreamWaves / stream_split(silu, rows, cols, outs, E);
-    return max_tiles(rows, E, kTile) * ((stream_groups(silu, outs) + teams - 1) / teams);
+    const int teams = kStreamWaves / stream_split(fp8, silu, rows, cols, outs, E);
+    return max_tiles(rows, E, stream_rows(fp8, rows, E)) * ((stream_groups(silu, outs) + teams - 1) / teams);
 }
 
 }  // namespace
 
-bool expert_launch_ok(bool silu, int rows, int cols, int outs, int E)
+bool expert_launch_ok(bool fp8, bool silu, int rows, int cols, int outs, int E)
 {
     // offsets within a tile are 32-bit; a grid dimension holds fewer than 2^32 threads
     if (cols > kMaxExpertCols || outs > (1 << 29)) return false;
     if (silu && (int64_t)outs * cols >= ((int64_t)1 << 35)) return false;
     const int64_t threads = expert_large(silu, rows, outs, E)
         ? tile_blocks(silu, rows, outs, E) * kTileWaves * kWave
-        : stream_blocks(silu, rows, cols, outs, E) * kStreamWaves * kWave;
+        : stream_blocks(fp8, silu, rows, cols, outs, E) * kStreamWaves * kWave;
     return threads < ((int64_t)1 << 32);
 }
 
@@ -759,17 +842,21 @@ hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int row
         else silu ? go(expert_tile_kernel<false, true>) : go(expert_tile_kernel<false, false>);
         return hipGetLastError();
     }
-    const int split = stream_split(silu, rows, cols, outs, E);
+    const int split = stream_split(fp8, silu, rows, cols, outs, E);
     const int groups = stream_groups(silu, outs), teams = kStreamWaves / split;
-    const dim3 grid((unsigned)stream_blocks(silu, rows, cols, outs, E));
+    const dim3 grid((unsigned)stream_blocks(fp8, silu, rows, cols, outs, E));
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(kStreamWaves * kWave), 0, stream, (const uint8_t*)x,
                            x_scales, rows, cols, expert_offset, E, w, w_scales, outs, out, groups, (groups + teams - 1) / teams);
     };
     auto pick = [&](auto sp) {
         constexpr int kS = decltype(sp)::value;
-        if (fp8) silu ? go(expert_stream_kernel<true, true, kS>) : go(expert_stream_kernel<true, false, kS>);
-        else silu ? go(expert_stream_kernel<false, true, kS>) : go(expert_stream_kernel<false, false, kS>);
+        if (fp8 && stream_rows(fp8, rows, E) < kTile)
+            silu ? go(expert_stream_kernel<true, true, kS, kTile / 2>) : go(expert_stream_kernel<true, false, kS, kTile / 2>);
+        else if (fp8)
+            silu ? go(expert_stream_kernel<true, true, kS, kTile>) : go(expert_stream_kernel<true, false, kS, kTile>);
+        else
+            silu ? go(expert_stream_kernel<false, true, kS, kTile>) : go(expert_stream_kernel<false, false, kS, kTile>);
     };
     if (split == 1) pick(std::integral_constant<int, 1>());
     else pick(std::integral_constant<int, kStreamWaves>());

@@ -580,8 +580,9 @@ int ep_dispatch_backward(const uint16_t* grad_recv, const int32_t* row_of_pair, 
  *   acc[r, n] = sum over the 128-column blocks b of
  *               (sum over c in b of x[r, c] * v(w[e][n, c]))
  *               * (w_scales[e][n, b] * x_scales[r, b])
- * in fp32, v the value of a code (the order of the sums depends on the sizes
- * only), and
+ * v the value of a code, every sum in fp32 (or exact: 16 products of fp8 rows
+ * at a time, of values below 2 and of values from 2 on) in an order that
+ * depends on the sizes only, and
  *   EP_ACT_NONE      out[r, n] = bf16_rne(acc[r, n]),  w has `outs` rows;
  *   EP_ACT_SILU_MUL  out[r, n] = bf16_rne(g / (1 + exp(-g)) * u) with
  *                    g = acc[r, n], u = acc[r, outs + n],  w has 2 * outs rows
