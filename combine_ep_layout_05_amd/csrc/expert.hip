@@ -51,6 +51,7 @@
 #include "ep_device.h"
 #include "ep_launch.h"
 #include "ep_numerics.h"
+#include "expert_plan.h"
 
 namespace ep {
 namespace {
@@ -61,7 +62,8 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
-constexpr int kTile = 16;
+static_assert(kStreamWaves * kWave == kExpertThreads && kTileWaves * kWave == kExpertThreads, "one workgroup size");
+static_assert(kExpertXcds == kXcds, "the plan has no device header");
 constexpr int kMaxExpertCols = 1 << 23;      // 64 rows of bf16 within 31-bit offsets
 constexpr int64_t kMaxBuffer = 0x7FFFFFFF;
 
@@ -190,9 +192,6 @@ __device__ __forceinline__ v4i load_b128(__amdgpu_buffer_rsrc_t r, int lane_offs
 // of LDS, transposed.  Nontemporal code loads drop a line between its two
 // halves here (5.5 -> 4.7 TB/s), and a team that goes on to further weight rows
 // gains nothing on more, shorter workgroups (4.9 -> 5.6 TB/s).
-constexpr int kStreamWaves = 4;
-constexpr int kStreamManyGroups = 2048, kStreamLongCols = 4096;
-constexpr int kGroupRows = 64;                    // weight rows per group: 4 operand tiles
 constexpr int kGroupTiles = kGroupRows / kTile;
 constexpr int kWindow = 16;                       // blocks whose scales are in LDS
 constexpr int kScalePitch = kGroupRows + kTile + 4;   // weight rows, then fp8 rows
@@ -202,7 +201,7 @@ constexpr int kScalePitch = kGroupRows + kTile + 4;   // weight rows, then fp8 r
 // instruction (lanes m and m + 8), whose sums are joined at the end.  kRows 16:
 // two instructions.
 template <bool kFp8, bool kSilu, int kSplit, int kRows>
-__global__ __launch_bounds__(kStreamWaves * kWave, kRows < kTile ? 4 : 3) void expert_stream_kernel(
+__global__ __launch_bounds__(kExpertThreads, kRows < kTile ? 4 : 3) void expert_stream_kernel(
     const uint8_t* __restrict__ x, const float* __restrict__ xs, int rows, int cols,
     const int32_t* __restrict__ off, int E, const uint8_t* __restrict__ w,
     const float* __restrict__ ws, int outs, uint16_t* __restrict__ out, int n_groups,
@@ -391,16 +390,10 @@ __global__ __launch_bounds__(kStreamWaves * kWave, kRows < kTile ? 4 : 3) void e
 // waves wait together); codes straight to registers in operand order 1.84 ms;
 // codes two stages ahead 1.67 ms; whole tiles of all experts before the rests
 // 1.80 ms (long and memory-bound tiles then no longer overlap).
-constexpr int kTileWaves = 4;
-constexpr int kTileRows = 64;                    // rows per workgroup
 constexpr int kRowTiles = kTileRows / kTile;
-constexpr int kWaveCols = 64;                    // weight rows per wave: 4 operand tiles
 constexpr int kColTiles = kWaveCols / kTile;
 constexpr int kStageBlocks = 2;
 constexpr int kCodeLoads = kWaveCols * kStageBlocks * 64 / 1024;                       // per wave
-// Row tiles that run together on an XCD and share codes and rows in its L2 (1,
-// 2, 4, 8: 1.74, 1.66, 1.62, 1.74 ms at the size above).
-constexpr int kChunkTiles = 4;
 constexpr int kScaleBlocks = 4;                  // blocks per load of scales
 
 template <bool kFp8> struct TileShared {
@@ -439,7 +432,7 @@ __device__ __forceinline__ void stage_barrier()
 }
 
 template <bool kFp8, bool kSilu>
-__global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
+__global__ __launch_bounds__(kExpertThreads, 2) void expert_tile_kernel(
     const uint8_t* __restrict__ x, const float* __restrict__ xs, int rows, int cols,
     const int32_t* __restrict__ off, int E, const uint8_t* __restrict__ w,
     const float* __restrict__ ws, int outs, uint16_t* __restrict__ out, int n_groups)
@@ -745,85 +738,12 @@ __global__ __launch_bounds__(kTileWaves * kWave, 2) void expert_tile_kernel(
 
 }  // namespace
 
-namespace {
-
-// Row tiles of the given height a batch can have: at most one partly filled
-// tile per expert that has rows.
-int64_t max_tiles(int rows, int E, int height)
-{
-    return (int64_t)rows / height + (rows < E ? rows : E);
-}
-
-int tile_groups(bool silu, int outs)
-{
-    const int per = kTileWaves * (silu ? kWaveCols / 2 : kWaveCols);
-    return (int)(((int64_t)outs + per - 1) / per);
-}
-
-// Which kernel a batch runs, by its rows per expert (the routing is on the
-// device, so by their average).  Measured on MI355X, streaming / tiles, gate
-// and up products of 4096 columns:
-//   32 experts x 2 x 2048 weight rows (512 workgroups of tiles), fp8 rows: 39 /
-//   45 us at 1 row per expert, 51 / 47 at 2, 57 / 49 at 8, 113 / 54 at 32; bf16:
-//   40 / 48, 53 / 49, 69 / 50, 149 / 66;
-//   8 experts (128 workgroups, half the CUs), fp8: 16 / 37 at 8, 32 / 45 at 32,
-//   54 / 53 at 64; bf16: 41 / 58 at 32, 69 / 70 at 64.
-bool expert_large(bool silu, int rows, int outs, int E)
-{
-    const bool fill = (int64_t)E * tile_groups(silu, outs) >= 2 * kCUs;
-    return rows >= (fill ? 2 : 64) * (int64_t)E;
-}
-
-int64_t tile_blocks(bool silu, int rows, int outs, int E)
-{
-    const int64_t tiles = max_tiles(rows, E, kTileRows);
-    constexpr int kRound = kXcds * kChunkTiles;
-    return (tiles + kRound - 1) / kRound * kRound * tile_groups(silu, outs);
-}
-
-int stream_groups(bool silu, int outs)
-{
-    const int per = silu ? kGroupRows / 2 : kGroupRows;
-    return (int)(((int64_t)outs + per - 1) / per);
-}
-
-// Rows per team of the streaming kernel: 16, or 8 where fp8 rows are few and the
-// two parts of all of them fit one matrix instruction, which leaves registers
-// for a fourth wave per SIMD.  4096 columns x 2 x 2048, 8 / 16: 29.3 / 32.4 us
-// with 24 experts of 1 row, 29.0 / 31.5 with 16 of 2, 277 / 281 with 288 of 1,
-// otherwise the same up to 2 rows; with 8 experts 19.7 / 16.3 at 4 rows, 23.5 /
-// 16.6 at 8, 56 / 33 at 32 (each team reads the codes again).
-int stream_rows(bool fp8, int rows, int E) { return fp8 && rows < 3 * (int64_t)E ? kTile / 2 : kTile; }
-
-// Waves that share a group in the streaming kernel: all four when the columns
-// are many or there are few groups, else one.  Measured (1 / 4 waves): 288 rows
-// on 288 experts, 2048 columns x 7168 bf16 259 / 306 us, 4096 columns x 2 x 2048
-// fp8 292 / 277, 7168 columns 527 / 487; 32 rows on 32 experts, 2048 x 6144 (3264
-// groups) 45 / 48; 16 rows on 16 experts, 2048 x 2048 (544 groups) 15 / 10; one
-// token, 8 experts, 6144 columns 32 / 21.
-int stream_split(bool fp8, bool silu, int rows, int cols, int outs, int E)
-{
-    const bool many = max_tiles(rows, E, stream_rows(fp8, rows, E)) * stream_groups(silu, outs) >= kStreamManyGroups;
-    return many && cols < kStreamLongCols ? 1 : kStreamWaves;
-}
-
-int64_t stream_blocks(bool fp8, bool silu, int rows, int cols, int outs, int E)
-{
-    const int teams = kStreamWaves / stream_split(fp8, silu, rows, cols, outs, E);
-    return max_tiles(rows, E, stream_rows(fp8, rows, E)) * ((stream_groups(silu, outs) + teams - 1) / teams);
-}
-
-}  // namespace
-
 bool expert_launch_ok(bool fp8, bool silu, int rows, int cols, int outs, int E)
 {
     // offsets within a tile are 32-bit; a grid dimension holds fewer than 2^32 threads
     if (cols > kMaxExpertCols || outs > (1 << 29)) return false;
     if (silu && (int64_t)outs * cols >= ((int64_t)1 << 35)) return false;
-    const int64_t threads = expert_large(silu, rows, outs, E)
-        ? tile_blocks(silu, rows, outs, E) * kTileWaves * kWave
-        : stream_blocks(fp8, silu, rows, cols, outs, E) * kStreamWaves * kWave;
-    return threads < ((int64_t)1 << 32);
+    return expert_plan(fp8, silu, rows, cols, outs, E).workgroups * kExpertThreads < ((int64_t)1 << 32);
 }
 
 hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int rows, int cols,
@@ -831,34 +751,28 @@ hipError_t launch_expert(const void* x, const float* x_scales, bool fp8, int row
                          const float* w_scales, int outs, bool silu, uint16_t* out,
                          hipStream_t stream)
 {
-    if (expert_large(silu, rows, outs, E)) {
-        const dim3 grid((unsigned)tile_blocks(silu, rows, outs, E));
-        auto go = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, grid, dim3(kTileWaves * kWave), 0, stream, (const uint8_t*)x,
-                               x_scales, rows, cols, expert_offset, E, w, w_scales, outs, out,
-                               tile_groups(silu, outs));
-        };
+    const ExpertPlan p = expert_plan(fp8, silu, rows, cols, outs, E);
+    auto go = [&](auto kernel, auto... more) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)p.workgroups), dim3(kExpertThreads), 0, stream,
+                           (const uint8_t*)x, x_scales, rows, cols, expert_offset, E, w, w_scales,
+                           outs, out, p.groups, more...);
+    };
+    if (p.tiles) {
         if (fp8) silu ? go(expert_tile_kernel<true, true>) : go(expert_tile_kernel<true, false>);
         else silu ? go(expert_tile_kernel<false, true>) : go(expert_tile_kernel<false, false>);
         return hipGetLastError();
     }
-    const int split = stream_split(fp8, silu, rows, cols, outs, E);
-    const int groups = stream_groups(silu, outs), teams = kStreamWaves / split;
-    const dim3 grid((unsigned)stream_blocks(fp8, silu, rows, cols, outs, E));
-    auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, dim3(kStreamWaves * kWave), 0, stream, (const uint8_t*)x,
-                           x_scales, rows, cols, expert_offset, E, w, w_scales, outs, out, groups, (groups + teams - 1) / teams);
-    };
-    auto pick = [&](auto sp) {
-        constexpr int kS = decltype(sp)::value;
-        if (fp8 && stream_rows(fp8, rows, E) < kTile)
-            silu ? go(expert_stream_kernel<true, true, kS, kTile / 2>) : go(expert_stream_kernel<true, false, kS, kTile / 2>);
+    auto pick = [&](auto split) {
+        constexpr int kS = decltype(split)::value, kHalf = kTile / 2;
+        const int parts = p.parts;
+        if (fp8 && p.rows == kHalf)
+            silu ? go(expert_stream_kernel<true, true, kS, kHalf>, parts) : go(expert_stream_kernel<true, false, kS, kHalf>, parts);
         else if (fp8)
-            silu ? go(expert_stream_kernel<true, true, kS, kTile>) : go(expert_stream_kernel<true, false, kS, kTile>);
+            silu ? go(expert_stream_kernel<true, true, kS, kTile>, parts) : go(expert_stream_kernel<true, false, kS, kTile>, parts);
         else
-            silu ? go(expert_stream_kernel<false, true, kS, kTile>) : go(expert_stream_kernel<false, false, kS, kTile>);
+            silu ? go(expert_stream_kernel<false, true, kS, kTile>, parts) : go(expert_stream_kernel<false, false, kS, kTile>, parts);
     };
-    if (split == 1) pick(std::integral_constant<int, 1>());
+    if (p.split == 1) pick(std::integral_constant<int, 1>());
     else pick(std::integral_constant<int, kStreamWaves>());
     return hipGetLastError();
 }

@@ -1,0 +1,116 @@
+"""Every kernel that ep_expert_w4 chooses from, against its definition in 64
+bits: the cases name the kernel they are meant for, and the library's own rule
+(csrc/expert_plan.h, compiled here for the CPU) has to choose it."""
+import ctypes
+import os
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+from tests import opsref
+from tests.test_gpu_expert import run
+from tests.test_gpu_expert_sums import check_sums
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+WRAPPER = """
+#include "expert_plan.h"
+extern "C" void plan(int fp8, int silu, int rows, int cols, int outs, int E, long long* p)
+{
+    const ep::ExpertPlan x = ep::expert_plan(fp8, silu, rows, cols, outs, E);
+    p[0] = x.tiles; p[1] = x.rows; p[2] = x.split; p[3] = x.groups; p[4] = x.parts; p[5] = x.workgroups;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    d = tmp_path_factory.mktemp("plan")
+    (d / "plan.cpp").write_text(WRAPPER)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I",
+                    os.path.join(ROOT, "combine_ep_layout_05_amd", "csrc"), str(d / "plan.cpp"),
+                    "-o", str(d / "plan.so")], check=True)
+    lib = ctypes.CDLL(str(d / "plan.so"))
+
+    def f(fp8, act, rows, cols, outs, E):
+        p = (ctypes.c_longlong * 6)()
+        lib.plan(int(fp8), int(act == "silu_mul"), rows, cols, outs, E, p)
+        return dict(zip(("tiles", "rows", "split", "groups", "parts", "workgroups"), p))
+    return f
+
+
+SPARE = 3          # rows behind the batch; they count in the rule as masked entries do
+# kernel, fp8, act, cols, outs, rows per expert
+CASES = {}
+for act, many, wide in (("none", 1032, 8200), ("silu_mul", 520, 4104)):
+    for fp8 in (True, False):
+        t = ("fp8_" if fp8 else "bf16_") + act
+        few = "stream8" if fp8 else "stream16"                  # up to 2 rows per expert
+        # one wave per group: many experts of 0 to 2 rows; 19 blocks: a second, clamped window of
+        # scales; few experts of many rows
+        CASES["one_wave_" + t] = (few, 1, fp8, act, 384, many, [0, 1, 2, 1, 0, 1, 2, 0, 1, 2] * 15)
+        CASES["one_wave_second_window_" + t] = (few, 1, fp8, act, 2432, wide,
+                                                [0] * 5 + [1, 0, 9, 0, 0, 3] + [0] * 5)
+        CASES["one_wave_deep_" + t] = ("stream16", 1, fp8, act, 384, wide, [60, 40, 80, 30])
+        # four waves per group, each with more than 16 blocks: even and odd
+        CASES["four_waves_second_window_" + t] = (few, 4, fp8, act, 8448, 40, [1, 0, 2, 0, 0, 1])
+        CASES["four_waves_second_window_odd_" + t] = ("stream16", 4, fp8, act, 8576, 72, [17, 0, 5])
+        # more row tiles than run together, in several groups of weight rows
+        CASES["chunks_" + t] = ("tiles", 0, fp8, act, 384, 600 if act == "none" else 328,
+                                [900, 0, 700, 650, 77, 3, 128, 64])
+
+
+def make(fp8, act, cols, outs, counts, seed):
+    g = np.random.default_rng(seed)
+    E, n, blocks = len(counts), int(sum(counts)) + SPARE, cols // 128
+    N = 2 * outs if act == "silu_mul" else outs
+    s = dict(off=np.concatenate([[0], np.cumsum(counts)]).astype(np.int32),
+             codes=g.integers(0, 256, size=(E, N, cols // 2), dtype=np.uint8),
+             scales=(g.uniform(0.5, 1.5, size=(E, N, blocks)) * 0.4 / np.sqrt(cols)).astype(np.float32))
+    if fp8:
+        by = g.integers(0, 0x69, size=(n, cols), dtype=np.uint8)
+        s["x"] = by | g.integers(0, 2, size=by.shape, dtype=np.uint8) << 7
+        s["xs"] = g.uniform(0.005, 0.02, size=(n, blocks)).astype(np.float32)
+        s["xv"] = opsref.e4m3(s["x"]) * np.repeat(s["xs"].astype(np.float64), 128, axis=1)
+    else:
+        t = torch.from_numpy(g.standard_normal((n, cols)).astype(np.float32)).to(torch.bfloat16)
+        s["x"], s["xs"], s["xv"] = t, None, t.double().numpy()
+    return s
+
+
+def form(p):
+    return ("tiles" if p["tiles"] else "stream%d" % p["rows"], p["split"])
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_cases_reach_their_kernels(plan, name):
+    kernel, split, fp8, act, cols, outs, counts = CASES[name]
+    p = plan(fp8, act, sum(counts) + SPARE, cols, outs, len(counts))
+    assert form(p) == (kernel, split), p
+    blocks = cols // 128
+    if "second_window" in name:              # blocks of the first wave, in pairs
+        assert ((blocks + 1) // 2 + split - 1) // split * 2 > 16
+    if kernel == "tiles":
+        assert sum((c + 63) // 64 for c in counts) > 32 and p["groups"] > 1
+    elif split == 1:
+        assert outs % (64 if act == "none" else 32) != 0         # a ragged last group
+
+
+def test_every_kernel_is_reached():
+    reached = {(c[0], c[1], c[2], c[3]) for c in CASES.values()}
+    for act in ("none", "silu_mul"):
+        for split in (1, 4):
+            assert {("stream8", split, True, act), ("stream16", split, True, act),
+                    ("stream16", split, False, act)} <= reached
+        assert {("tiles", 0, True, act), ("tiles", 0, False, act)} <= reached
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_products(name):
+    kernel, split, fp8, act, cols, outs, counts = CASES[name]
+    print("expert plan %s: %s/%d C=%d D=%d" % (name, kernel, split, cols, outs), flush=True)
+    s = make(fp8, act, cols, outs, counts, seed=cols + outs)
+    check_sums(s, run(s, outs, act, fp8), act)
