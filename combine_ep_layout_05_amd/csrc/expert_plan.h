@@ -43,17 +43,31 @@ inline int64_t expert_row_tiles(int rows, int E, int height)
 inline int expert_groups(int outs, int per) { return (int)(((int64_t)outs + per - 1) / per); }
 
 // Which kernel a batch runs, by its rows per expert (the routing is on the
-// device, so by their average).  Measured on MI355X, streaming / tiles, gate
-// and up products of 4096 columns:
-//   32 experts x 2 x 2048 weight rows (512 workgroups of tiles), fp8 rows: 39 /
-//   46 us at 1 row per expert, 52 / 47 at 2, 59 / 50 at 8, 119 / 65 at 32; bf16:
-//   40 / 47, 54 / 48, 69 / 50, 149 / 67;
-//   8 experts (128 workgroups, half the CUs), fp8: 17 / 38 at 8, 33 / 58 at 32,
-//   56 / 70 at 64; bf16: 41 / 58 at 32, 71 / 71 at 64.
-inline bool expert_large(int rows, int groups, int E)
+// device, so by their average).  The streaming kernel asks for an expert's codes
+// again for every 16 rows, the tile kernel for every 64, but a workgroup of
+// tiles takes its time however few there are: the fewer workgroups (experts x
+// groups of weight rows), the more rows it takes to pay.  Measured on MI355X, gate
+// and up products of 4096 columns, 2 x 2048 weight rows (16 groups), streaming /
+// tiles, us:
+//   experts  fp8 rows, by rows per expert               bf16 rows
+//    1       64: 11.5 / 63, 512: 51 / 67                64: 12 / 62, 512: 65 / 68
+//    4       64: 34 / 67, 128: 56 / 67, 256: 101 / 71   64: 42 / 68, 128: 70 / 67
+//    8       32: 33 / 58, 64: 56 / 70                   32: 42 / 58, 64: 71 / 71
+//   16       16: 43 / 51, 32: 64 / 60, 64: 105 / 73     16: 52 / 53, 32: 80 / 61
+//   24       4: 44 / 46, 8: 46 / 46, 32: 92 / 63        4: 46 / 47, 8: 54 / 47
+//   31       1: 37 / 45, 2: 48 / 46, 32: 117 / 64       2: 50 / 48, 32: 145 / 67
+//   32       1: 39 / 46, 2: 52 / 47, 32: 119 / 65       1: 40 / 47, 2: 54 / 48
+// Short columns: 18 experts, 1024 x 7168 (28 groups), 8: 17 / 24, 32: 35 / 37, 64:
+// 58 / 44; 64 experts, 1024 x 2 x 256 (2 groups), 16: 10 / 12, 32: 15 / 15, 64: 23
+// / 17.  Of 212 such points the rule takes the slower kernel by more than 14 % at
+// 3: bf16 rows on 18 experts, 7168 x 2 x 1024, 32 rows (34 %), and 8 experts, 4096
+// x 2 x 512, 256 rows (fp8 25, bf16 58 %).
+inline bool expert_large(int rows, int cols, int groups, int E)
 {
-    const bool fill = (int64_t)E * groups >= 512;
-    return rows >= (fill ? 2 : 64) * (int64_t)E;
+    const int64_t w = (int64_t)E * groups;
+    if (w >= 512) return rows >= 2 * (int64_t)E;
+    if (cols < 2048) return rows >= 32 * (int64_t)E;
+    return rows * w >= E * (2 * w + 24 * (512 - w));      // 2 + 24 (512 / w - 1) rows per expert
 }
 
 // Rows per team of the streaming kernel: 16, or 8 where fp8 rows are few and the
@@ -83,7 +97,7 @@ inline ExpertPlan expert_plan(bool fp8, bool silu, int rows, int cols, int outs,
     ExpertPlan p{};
     const int parts = silu ? 2 : 1;                             // gate and up rows
     p.groups = expert_groups(outs, kTileWaves * kWaveCols / parts);
-    p.tiles = expert_large(rows, p.groups, E);
+    p.tiles = expert_large(rows, cols, p.groups, E);
     if (p.tiles) {
         constexpr int kRound = kExpertXcds * kChunkTiles;
         p.rows = kTileRows;

@@ -44,7 +44,7 @@ def plan(tmp_path_factory):
 SPARE = 3          # rows behind the batch; they count in the rule as masked entries do
 # kernel, fp8, act, cols, outs, rows per expert
 CASES = {}
-for act, many, wide in (("none", 1032, 8200), ("silu_mul", 520, 4104)):
+for act, many, wide, wider in (("none", 1032, 8200, 12296), ("silu_mul", 520, 4104, 6152)):
     for fp8 in (True, False):
         t = ("fp8_" if fp8 else "bf16_") + act
         few = "stream8" if fp8 else "stream16"                  # up to 2 rows per expert
@@ -53,13 +53,18 @@ for act, many, wide in (("none", 1032, 8200), ("silu_mul", 520, 4104)):
         CASES["one_wave_" + t] = (few, 1, fp8, act, 384, many, [0, 1, 2, 1, 0, 1, 2, 0, 1, 2] * 15)
         CASES["one_wave_second_window_" + t] = (few, 1, fp8, act, 2432, wide,
                                                 [0] * 5 + [1, 0, 9, 0, 0, 3] + [0] * 5)
-        CASES["one_wave_deep_" + t] = ("stream16", 1, fp8, act, 384, wide, [60, 40, 80, 30])
+        CASES["one_wave_deep_" + t] = ("stream16", 1, fp8, act, 384, wider, [40, 20, 35, 25])
         # four waves per group, each with more than 16 blocks: even and odd
         CASES["four_waves_second_window_" + t] = (few, 4, fp8, act, 8448, 40, [1, 0, 2, 0, 0, 1])
         CASES["four_waves_second_window_odd_" + t] = ("stream16", 4, fp8, act, 8576, 72, [17, 0, 5])
         # more row tiles than run together, in several groups of weight rows
         CASES["chunks_" + t] = ("tiles", 0, fp8, act, 384, 600 if act == "none" else 328,
                                 [900, 0, 700, 650, 77, 3, 128, 64])
+        # long columns, an odd and an even number of blocks; tiles of every number of row groups
+        CASES["tiles_long_odd_" + t] = ("tiles", 0, fp8, act, 2176, 3400 if act == "none" else 1704,
+                                        [0, 130, 0, 0, 65, 1, 17, 48] + [0] * 32)
+        CASES["tiles_long_" + t] = ("tiles", 0, fp8, act, 2304, 3400 if act == "none" else 1704,
+                                    [33, 0, 0, 64, 0, 2, 0, 81] + [0] * 32)
 
 
 def make(fp8, act, cols, outs, counts, seed):
@@ -92,10 +97,30 @@ def test_cases_reach_their_kernels(plan, name):
     blocks = cols // 128
     if "second_window" in name:              # blocks of the first wave, in pairs
         assert ((blocks + 1) // 2 + split - 1) // split * 2 > 16
-    if kernel == "tiles":
+    if "chunks" in name:
         assert sum((c + 63) // 64 for c in counts) > 32 and p["groups"] > 1
     elif split == 1:
         assert outs % (64 if act == "none" else 32) != 0         # a ragged last group
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_choice_by_rows_and_workgroups(plan, fp8):
+    """The rule at measured points (gate and up of 2048, 4096 columns: 16 groups
+    per expert): few rows or few workgroups stream, and where the workgroups
+    of tiles come close to filling the GPU the choice does not jump."""
+    def tiles(E, per_expert, cols=4096, outs=2048, act="silu_mul"):
+        return bool(plan(fp8, act, E * per_expert, cols, outs, E)["tiles"])
+    for E, stream, tile in ((1, 512, 1024), (4, 128, 256), (8, 32, 128), (16, 16, 32), (24, 4, 16),
+                            (31, 2, 4), (32, 1, 2), (256, 1, 2)):
+        assert not tiles(E, stream) and tiles(E, tile), E
+    first = [next(r for r in range(1, 5000) if tiles(E, r)) for E in range(1, 40)]
+    assert first == sorted(first, reverse=True)                # more workgroups, fewer rows
+    assert first[30] <= first[31] + 1                          # 31 and 32 experts
+    assert not tiles(18, 16, 1024, 7168, "none") and tiles(18, 64, 1024, 7168, "none")
+    assert not tiles(64, 16, 1024, 256) and tiles(64, 64, 1024, 256)
+    # no overflow at the largest sizes the call takes
+    assert plan(fp8, "none", 2**31 - 1, 2**23, 8, 1024)["tiles"]
+    assert plan(fp8, "none", 2**31 - 1, 2**23, 8, 1)["workgroups"] > 0
 
 
 def test_every_kernel_is_reached():
