@@ -536,6 +536,8 @@ int ep_route(const void* logits, int dtype, int T, int E, int K, int score, cons
  * and 0 elsewhere; computed in fp32 and rounded once.  Every element is
  * written.  Entries whose id is negative or >= E take no part (their
  * grad_topk_w is not used); the terms of an expert named twice are added.
+ * The modes that sum over the choices read no other logits: a NaN elsewhere in
+ * the row, which makes ep_route's weights NaN, does not reach the gradient.
  * grad_logits must not overlap the inputs.
  * Errors: those of ep_route.
  */
@@ -604,7 +606,10 @@ int ep_dispatch_backward(const uint16_t* grad_recv, const int32_t* row_of_pair, 
  * NULL or misaligned pointers (x, w, out 16 B, the rest 4 B) when rows > 0,
  * or sizes past the kernels' offsets and grids: cols > 2^23, outs > 2^29,
  * outs * cols >= 2^35 with EP_ACT_SILU_MUL, or a launch of 2^32 threads or
- * more (from about rows * outs = 2^38 on).
+ * more.  With m = min(rows, E) a launch is below that where
+ *   (rows / 64 + m + 32) * (outs + 256) < 2^32  and
+ *   (rows / 8 + m) * (outs + 64) < 2^30         (with EP_ACT_SILU_MUL half of
+ * both); beyond, it depends on which of the two kernels the sizes choose.
  */
 #define EP_ACT_NONE 0
 #define EP_ACT_SILU_MUL 1

@@ -132,6 +132,38 @@ def test_every_kernel_is_reached():
         assert {("tiles", 0, True, act), ("tiles", 0, False, act)} <= reached
 
 
+def test_launch_limits(plan):
+    """Sizes that ep.h says are taken have launches below 2^32 threads; where the
+    launch is larger the call refuses."""
+    import combine_ep_layout_05_amd as ep
+    fake = ctypes.c_void_p(0x10000)                    # never dereferenced: refused before
+
+    def rc(payload, rows, cols, E, outs, act):
+        return ep._lib.ep_expert_w4(fake, fake, payload, rows, cols, fake, E, fake, fake, outs, act,
+                                    fake, None)
+    g = np.random.default_rng(0)
+    over = under = 0
+    for _ in range(4000):
+        rows, E = int(2 ** g.uniform(0, 31)) - 1, int(2 ** g.uniform(0, 10.01))
+        outs, cols = int(2 ** g.uniform(3, 26)) // 8 * 8, 128 * int(2 ** g.uniform(0, 9))
+        fp8, silu = bool(g.integers(2)), int(g.integers(2))
+        threads = plan(fp8, "silu_mul" if silu else "none", rows, cols, outs, E)["workgroups"] * 256
+        m = min(rows, E)
+        taken = (rows // 64 + m + 32) * (outs + 256) < 2 ** (32 - silu) and \
+            (rows // 8 + m) * (outs + 64) < 2 ** (30 - silu)
+        if taken:
+            assert threads < 2 ** 32
+            under += 1
+        if threads >= 2 ** 32:
+            assert rc(0 if fp8 else 1, rows, cols, E, outs, silu) == -1
+            over += 1
+    assert over > 200 and under > 200
+    # streaming, 4 waves per group: refused well below 2^38 elements of output
+    p = plan(True, "none", 1024, 4096, 1 << 20, 1024)
+    assert not p["tiles"] and p["workgroups"] * 256 >= 2 ** 32
+    assert rc(0, 1024, 4096, 1024, 1 << 20, 0) == -1
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", sorted(CASES))
 def test_products(name):
