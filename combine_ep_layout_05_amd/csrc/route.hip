@@ -385,6 +385,14 @@ void route_backward_launch(const void* logits, int T, int E, int K, bool sigmoid
 }
 
 // Calls f(lanes, logits per lane) with the smallest instance that holds E logits.
+// Besides the powers of two there is one of 5 (257 to 320 experts with 64 lanes,
+// 65 to 80 with 16).  Measured with 5 / 6 / 8 logits per lane, top-8 of 288
+// experts in fp32, graphs of 50 launches: 128 tokens 3.8 / 4.0 / 3.9 us, with a
+// bias 5.9 / 6.5 / 6.6, 16384 tokens 15.6 / 16.7 / 18.4, with a bias 29 / 33 / 39,
+// full softmax gradient 16.1 / 17.8 / 17.0; the renormalised gradient alone is
+// slower, 13.1 / 14.7 / 11.4 (its stores are not vectors).  One of 6 for 321 to
+// 384 would serve a bias at many tokens (16384 x 384 34 for 39 us) and cost the
+// fp32 gradients more (17.4 for 11.8).
 template <class F>
 void with_shape(bool narrow, int E, F&& f)
 {
