@@ -263,3 +263,46 @@ def test_missing_outputs_on_a_stream_beside_a_busy_one():
         torch.cuda.synchronize()
         for t, e in zip(got, (ey, ew, ex)):
             assert torch.equal(t, e)
+
+
+def test_dedup_combine_backward():
+    """ep_combine_backward is the gradient of the two dedup levels together:
+    against torch's gradients, in 64 bits, of the partials and their sum, over
+    the tables of the dedup layout.  (Tokens with several experts of one
+    partition, masked entries and a token without any.)"""
+    ep = ep_()
+    T, H, K, E, P = 41, 520, 8, 32, 8
+    g = np.random.default_rng(18)
+    idx_h = g.integers(-1, E, size=(T, K)).astype(np.int32)
+    idx_h[7] = -1
+    idx = torch.from_numpy(idx_h).cuda()
+    b = ep.EpBuffers(T, H, K, E, P, payload="bf16")
+    d = ep.EpDedupBuffers(T, H, K, E, P, payload="bf16")
+    b.layout(idx)
+    d.layout(idx)
+    tg = torch.Generator(device="cuda").manual_seed(3)
+    go, y = (torch.randn(r, H, device="cuda", generator=tg, dtype=torch.bfloat16) for r in (T, T * K))
+    w = torch.rand(T, K, device="cuda", generator=tg)
+    d.combine_partial(y, b.row_of_pair, w)
+    out = d.combine_reduce()
+    gy, gw = b.combine_backward(go, y, w)
+    torch.cuda.synchronize()
+
+    row = b.row_of_pair.long().reshape(T, K)
+    assert int((row >= 0).sum()) > int((d.tp_row >= 0).sum()) > T       # shared copies
+    yd, wd = y.double().requires_grad_(), w.double().requires_grad_()
+    terms = wd[:, :, None] * yd[row.clamp_min(0)]
+    bit = 1 << torch.arange(K, device="cuda")
+    in_part = (d.kmask.reshape(T, P, 1) & bit) != 0                     # [T, P, K]
+    in_part &= (d.tp_row.reshape(T, P, 1) >= 0) & (row >= 0)[:, None]
+    partial = torch.where(in_part[..., None], terms[:, None], 0.0).sum(2)
+    ref = partial.sum(1)
+    # forward: each partial rounded to bf16, then their sum (half a step, 2^-8 each)
+    lim = 2.0 ** -8 * (partial.abs().sum(1) + ref.abs()) * (1 + 2.0 ** -7) + 1e-30
+    assert bool(((out.double() - ref).abs() <= lim).all())
+    ref.backward(go.double())
+    # bf16 rows: one fp32 product, rounded; weights: H/256 + 32 additions of fp32 terms
+    assert bool(((gy.double() - yd.grad).abs() <= (2.0 ** -8 + 2.0 ** -23) * yd.grad.abs()).all())
+    mag = (go.double()[:, None].abs() * y.double()[row.clamp_min(0)].abs()).sum(2)
+    assert bool(((gw.double() - wd.grad).abs() <= (H / 256 + 32) * 2.0 ** -24 * mag).all())
+    assert bool((gw[row < 0] == 0).all())
