@@ -817,7 +817,8 @@ class EpBuffers:
 
     def route(self, logits, score="softmax", bias=None, renorm=True, scale=1.0, stream=None):
         """logits fp32 or bf16 [n, E], n <= T -> (topk_idx[:n], topk_w[:n]) of
-        these buffers, as the layout and the combine take them (ep_route)."""
+        these buffers, as the layout and the combine take them (ep_route); the
+        next call overwrites them."""
         if logits.dim() != 2 or logits.shape[0] > self.T or logits.shape[1] != self.E:
             raise ValueError("logits: expected [n, %d] with n <= %d, got %s" % (
                 self.E, self.T, tuple(logits.shape)))
@@ -828,7 +829,8 @@ class EpBuffers:
 
     def combine_backward(self, grad_out, expert_out, topk_w, grad_expert_out=None,
                          grad_topk_w=None, stream=None):
-        """The combine's gradient for the current batch: grad_out bf16 [n, H] ->
+        """The combine's gradient for the current batch (the last layout's: layers
+        whose backward passes come later need buffers each): grad_out bf16 [n, H] ->
         (grad_expert_out bf16 [n*K, H], grad_topk_w fp32 [n, K]).  Outputs not
         given are allocated on the call's stream, grad_expert_out as zeros (rows
         without a pair are not written); give them when the call is captured

@@ -33,7 +33,7 @@
 // us for down (2048 columns, 7168 rows; 6.0 TB/s); one token, 8 experts, 6144
 // columns, 2 x 2048 rows 21.5 us (5.0 TB/s).  At 128 rows per expert (4096 tokens,
 // Zipf routing) gate and up take 2.17 ms with fp8 rows (0.89 PFLOP/s) and 2.23
-// ms with bf16 (0.86 PFLOP/s): twice 32 and four times 16 cycles of the matrix
+// ms with bf16 (0.86 PFLOP/s; on another box 2.22 and 2.30): twice 32 and four times 16 cycles of the matrix
 // unit per 16 x 16 outputs and block (1.5 ms in all at the rate a library product
 // reaches), beside 8 vector instructions that scale and add the result and, fp8,
 // 8 that part the rows.
@@ -385,7 +385,8 @@ __global__ __launch_bounds__(kExpertThreads, kRows < kTile ? 4 : 3) void expert_
 // The 16-byte pieces of a row in LDS are permuted (piece ^ row) so that 8
 // lanes reading one piece of 8 neighbouring rows meet 8 different banks.
 //
-// Also measured, 4096 tokens x 7168, gate and up, fp8: 128-row tiles in one
+// Also measured, 4096 tokens x 7168, gate and up, fp8, with one matrix instruction
+// per block (whole rows, 1.54 ms): 128-row tiles in one
 // workgroup of 8 waves a CU 1.69 ms (nothing overlaps its prologue, and the
 // waves wait together); codes straight to registers in operand order 1.84 ms;
 // codes two stages ahead 1.67 ms; whole tiles of all experts before the rests
@@ -456,7 +457,8 @@ __global__ __launch_bounds__(kExpertThreads, 2) void expert_tile_kernel(
     const int64_t wrows = (int64_t)outs * kParts;
     // the expert's only tile: nobody else wants its codes in the L2, and loaded
     // nontemporally they come faster (512 tokens, 256 experts 434 -> 383 us; where
-    // tiles share them slower, 1.64 -> 1.81 ms at 4096 tokens)
+    // tiles share them slower, 1.64 -> 1.81 ms at 4096 tokens; both with one matrix
+    // instruction per block)
     const bool alone = off[expert + 1] - off[expert] <= kTileRows;
 
     // (past the last output: other rows or 0, not stored)
