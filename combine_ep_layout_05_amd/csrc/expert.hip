@@ -33,7 +33,7 @@
 // us for down (2048 columns, 7168 rows; 6.0 TB/s); one token, 8 experts, 6144
 // columns, 2 x 2048 rows 21.5 us (5.0 TB/s).  At 128 rows per expert (4096 tokens,
 // Zipf routing) gate and up take 2.17 ms with fp8 rows (0.89 PFLOP/s) and 2.23
-// ms with bf16 (0.86 PFLOP/s; on another box 2.22 and 2.30): twice 32 and four times 16 cycles of the matrix
+// ms with bf16 (0.86 PFLOP/s; on another card 2.22 and 2.30): twice 32 and four times 16 cycles of the matrix
 // unit per 16 x 16 outputs and block (1.5 ms in all at the rate a library product
 // reaches), beside 8 vector instructions that scale and add the result and, fp8,
 // 8 that part the rows.
