@@ -527,17 +527,34 @@ def ep_expert_w4(x, x_scales, expert_offset, w, w_scales, out, act="none", strea
 _E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 
 
+_W4_PIECE = 1 << 26                    # weights laid out at a time
+
+
 def w4_quantise(weight):
     """weight [..., C] of any float type, C % 128 == 0 -> (codes uint8
     [..., C/2], scales fp32 [..., C/128]) as ep_expert_w4 takes them: per 128
     columns scale = amax / 6, codes the nearest e2m1 value of weight / scale,
-    ties to the even code.  Plain torch, for laying weights out once."""
+    ties to the even code.  Plain torch, for laying weights out once, in pieces
+    of 2^26 weights: the intermediates of a piece take about 2 GiB."""
     if weight.dim() == 0 or weight.shape[-1] % SCALE_BLOCK:
         raise ValueError("weight: the last dimension must be a multiple of %d" % SCALE_BLOCK)
-    blocks = weight.float().unflatten(-1, (-1, SCALE_BLOCK))
+    C = weight.shape[-1]
+    lead = weight.shape[:-1]
+    rows = weight.reshape(-1, C)
+    codes = torch.empty((rows.shape[0], C // 2), dtype=torch.uint8, device=weight.device)
+    scales = torch.empty((rows.shape[0], C // SCALE_BLOCK), dtype=torch.float32, device=weight.device)
+    step = max(1, _W4_PIECE // max(C, 1))
+    for i in range(0, rows.shape[0], step):
+        codes[i:i + step], scales[i:i + step] = _w4_piece(rows[i:i + step])
+    return codes.reshape(*lead, C // 2), scales.reshape(*lead, C // SCALE_BLOCK)
+
+
+def _w4_piece(rows):
+    """w4_quantise of rows [n, C] at once."""
+    blocks = rows.float().unflatten(-1, (-1, SCALE_BLOCK))
     scales = blocks.abs().amax(-1) / _E2M1[-1]
     q = blocks / torch.where(scales > 0, scales, 1.0)[..., None]
-    mids = torch.tensor([(a + b) / 2 for a, b in zip(_E2M1, _E2M1[1:])], device=weight.device)
+    mids = torch.tensor([(a + b) / 2 for a, b in zip(_E2M1, _E2M1[1:])], device=rows.device)
     # at a midpoint between codes i and i+1 the even one is taken
     code = torch.bucketize(q.abs(), mids, right=False)
     tie = (code < 7) & (q.abs() == mids[code.clamp_max(6)]) & (code % 2 == 1)

@@ -337,3 +337,25 @@ def test_missing_outputs_are_made_on_the_calls_stream(fake_streams, monkeypatch)
             call()
     assert not [m for m in made if m[0].startswith("ep_") or m[0] in ("empty", "zeros_like", "empty_like")
                 and m[1] is s]
+
+
+def test_quantise_works_in_pieces(monkeypatch):
+    """Large weights are laid out piece by piece, with the same result: no
+    intermediate (of 8 bytes per weight) is as large as the weight."""
+    w = torch.randn(3, 37, 384)
+    assert w.numel() <= ep._W4_PIECE
+    whole = ep.w4_quantise(w)
+    largest = []
+    bucketize = torch.bucketize
+    monkeypatch.setattr(torch, "bucketize",
+                        lambda q, *a, **kw: largest.append(q.numel()) or bucketize(q, *a, **kw))
+    for piece in (1, 384, 5000):                       # a row at least, and pieces that end inside
+        monkeypatch.setattr(ep, "_W4_PIECE", piece)
+        del largest[:]
+        codes, scales = ep.w4_quantise(w)
+        assert torch.equal(codes, whole[0]) and torch.equal(scales, whole[1])
+        assert max(largest) <= max(piece, 384) and sum(largest) == w.numel()
+    view = torch.randn(384, 6).t()                     # not contiguous
+    assert torch.equal(ep.w4_quantise(view)[0], ep.w4_quantise(view.contiguous())[0])
+    empty = ep.w4_quantise(torch.zeros(0, 5, 256))
+    assert empty[0].shape == (0, 5, 128) and empty[1].shape == (0, 5, 2)
