@@ -8,7 +8,8 @@ import torch
 from tests import opsref
 from tests.test_gpu_expert import make, run
 
-# rows per expert: the streaming kernel (fewer than 2 on average, or few experts) and the tiles
+# rows per expert: up to 2048 columns "stream" and "stream_deep" take the streaming kernel, "tiles"
+# the tile kernel; with more all of them stream (test_gpu_expert_plans has long columns on tiles)
 COUNTS = {"stream": [0, 1, 3, 0, 1, 0, 0, 2, 0, 1], "stream_deep": [7, 8, 9, 0, 33],
           "tiles": [70, 1, 0, 130], "tiles_one": [300]}
 
